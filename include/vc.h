@@ -121,6 +121,7 @@ extern "C" {
 #define VC_MAX_HEAD_DIM 256
 #define VC_MAX_GQA_GROUP 8
 #define VC_MAX_VERIFY_QUERIES 64
+#define VC_MAX_TOP 64
 #define VC_STATIC_SCRATCH_BYTES (8u << 20)
 
 typedef enum {
@@ -133,6 +134,9 @@ typedef enum {
     VC_ERR_TIMEOUT = 6,     /* (device status) a bounded wait gave up             */
     VC_ERR_WORKSPACE = 7    /* workspace null or smaller than the size query      */
 } vc_status;
+
+/* Element types of arrays that come in more than one. */
+typedef enum { VC_F32 = 0, VC_BF16 = 1, VC_F16 = 2 } vc_dtype;
 
 typedef void *vc_stream_t; /* cudaStream_t */
 typedef void *vc_event_t;  /* cudaEvent_t  */
@@ -532,6 +536,181 @@ VC_API vc_status vc_swiglu(const float *gu, int32_t m, int32_t f, float *out, vc
 VC_API vc_status vc_rope_kv_write(const float *qkv, int32_t m, const int32_t *row_req, const int32_t *row_pos,
                                   int32_t num_q_heads, float rope_theta, void *q_out, const vc_paged_kv *full,
                                   int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * Rotary positions in general form.  The first rot_dim channels of a head
+ * turn in R/2 pairs (R = rot_dim), pair i by the angle position * f_i:
+ *   interleaved == 0: pair i = channels (i, i + R/2)
+ *   interleaved != 0: pair i = channels (2i, 2i + 1)
+ *   (a, b) -> amplitude * (a cos - b sin, b cos + a sin)
+ * and the other channels are copied.  Frequencies, for contexts longer than
+ * the one a model was trained on (factor s >= 1):
+ *   w_i = theta^(-2i/R)
+ *   original_len == 0: f_i = w_i / s                (every pair stretched)
+ *   original_len  > 0: f_i = w_i (g_i + (1 - g_i) / s),
+ *                      g_i = clamp((original_len w_i / 2pi - low_turns) /
+ *                                  (high_turns - low_turns), 0, 1)
+ *                      (pairs that turn often within original_len keep their
+ *                      frequency, pairs that do not complete low_turns are
+ *                      stretched by s, those between are blended)
+ * factor 1 leaves f_i = w_i.  f_i / 2pi is kept as a 64-bit binary fraction and
+ * multiplied by the position modulo 1: an angle is off by at most 2^-32 of a
+ * turn for positions below 2^22 (2^-24 of a turn at 2^31).
+ */
+typedef struct {
+    float theta;          /* >= 1                                         */
+    int32_t rot_dim;      /* even, 0 .. head_dim (0: nothing is rotated)  */
+    int32_t interleaved;
+    float factor;         /* >= 1                                         */
+    int32_t original_len; /* >= 0                                         */
+    float low_turns;      /* read when original_len > 0 and factor > 1:   */
+    float high_turns;     /*   low_turns < high_turns                     */
+    float amplitude;      /* finite; scales the rotated channels          */
+} vc_rotary;
+
+/*
+ * vc_rotary_kv_write -- rotate the Q and K heads of m rows and write their K
+ * and V (unrotated) into KV_full; the general form of vc_rope_kv_write, whose
+ * angle is always that of the cache slot: the nodes of a drafted tree share
+ * positions while each has a slot of its own.
+ *  qkv         device, qkv_dtype VC_F32 or VC_BF16: row r at qkv + r *
+ *              row_stride values, (Hq + 2 Hkv) heads of head_dim contiguous
+ *              channels (Q heads, K heads, V heads).
+ *              row_stride >= (Hq + 2 Hkv) head_dim.
+ *  row_req     device int32 [m]: request; -1 = a padding row, nothing of
+ *              which is read or written.
+ *  row_pos     device int32 [m]: position that sets the angle (>= 0).
+ *  row_slot    device int32 [m] or NULL (= row_pos): cache position written.
+ *              Rows of one call must name distinct (request, slot) pairs:
+ *              of two rows with the same pair either may be kept, in parts.
+ *  q_out       device bf16 [m][Hq][head_dim], written whole for each row.
+ *  full        bits == 16; seq_lens is not read.  head_dim a multiple of 32.
+ * A row whose request, position, slot or page is out of range is skipped
+ * whole and reported (VC_ERR_BAD_INDEX in dev_status).  Arithmetic in fp32,
+ * rounded once to bf16.  q_out and the pools must not overlap qkv.
+ */
+VC_API vc_status vc_rotary_kv_write(const void *qkv, int32_t qkv_dtype, int64_t row_stride, int32_t m,
+                                    const int32_t *row_req, const int32_t *row_pos, const int32_t *row_slot,
+                                    int32_t num_q_heads, const vc_rotary *rotary, void *q_out,
+                                    const vc_paged_kv *full, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * A tree of drafts.  A round may draft a tree of n_q <= 64 nodes instead of a
+ * chain: node 0 is the pending token (the last one emitted), every other node
+ * a drafted token that follows its parent, so several continuations are
+ * verified in one pass.  Node i of request b lies in KV_full at position
+ * base + i, base = seq_lens[b] - n_q: the tree is the last n_q entries, as the
+ * block of vc_verify_attn is.
+ *  parent   device int32 [batch][n_q]: index of the node that node i follows,
+ *           < i; -1 for a node that follows the prefix (node 0 always); less
+ *           than -1 for an absent node (trees of fewer nodes in a batch).
+ *
+ * vc_tree_plan -- what the nodes see and where they stand:
+ *  mask      device uint64 [batch][n_q]: bit j set when node j is node i or
+ *            one of its ancestors; 0 for an absent node
+ *  position  device int32 [batch][n_q]: base + depth (the number of
+ *            ancestors), the position that rotates the node; -1 when absent
+ * A parent >= i and a node that follows an absent one are absent, and
+ * reported (VC_ERR_BAD_INDEX in dev_status); so is every node of a request
+ * with seq_lens[b] < n_q.
+ */
+VC_API vc_status vc_tree_plan(const int32_t *parent, int32_t batch, int32_t n_q, const int32_t *seq_lens,
+                              uint64_t *mask, int32_t *position, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_tree_attn -- the verification pass of a tree over KV_full: node i of
+ * request b attends to the prefix (positions 0 .. base - 1) and to position
+ * base + j for every set bit j of mask[b][i].
+ *  q           device bf16 [batch][n_q][num_q_heads][head_dim]
+ *  mask        device uint64 [batch][n_q], of vc_tree_plan or any other; bits
+ *              from n_q on are not read.  0 leaves the row out: zeros.
+ *  out         device [batch][n_q][num_q_heads][head_dim], out_dtype VC_F32
+ *              or VC_BF16 (the probabilities enter the second product in bf16
+ *              either way, as in vc_verify_attn)
+ * Limits and the other arguments are vc_verify_attn's; softmax_scale > 0; the
+ * pools lie on 16-byte boundaries, q and out too.  A request with seq_lens[b] < n_q, or of
+ * more than max_seq_len, gets VC_ERR_BAD_INDEX in dev_status and zeros.
+ * Entries of the tree that a node does not attend to do not touch its result,
+ * whatever they hold (infinities and NaN included); a node that attends to an
+ * entry of the tree whose V holds one gets NaN in all channels.  The context
+ * is split evenly over the GPU, so the last bits of a result depend on the
+ * batch's lengths; they are the same from call to call.
+ */
+VC_API size_t vc_tree_workspace_bytes(const vc_paged_kv *full, int32_t n_q, int32_t num_q_heads,
+                                      int32_t max_seq_len);
+VC_API vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_paged_kv *full,
+                              const uint64_t *mask, float softmax_scale, void *out, int32_t out_dtype,
+                              int32_t max_seq_len, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                              vc_stream_t stream);
+
+/*
+ * vc_tree_accept -- greedy acceptance of a tree: from node 0 on, the child
+ * (the lowest index where several qualify) whose token is the verifier's
+ * prediction after the current node is accepted, until there is none.
+ *  tokens      device int32 [batch][n_q]: the nodes' tokens (node 0's is not read)
+ *  verified    device int32 [batch][n_q]: prediction after each node (the argmax
+ *              of vc_accept or of vc_token_logprobs)
+ *  accept_len  device int32 [batch]: accepted drafts a (0 .. n_q - 1); -1 for an
+ *              idle request, one whose node 0 is absent (parent other than -1)
+ *  path        device int32 [batch][n_q]: path[0] = 0, the accepted nodes in
+ *              order, -1 behind them
+ *  emitted     device int32 [batch][n_q]: the a accepted tokens, then
+ *              verified[path[a]]; -1 behind them
+ * For a chain (parent[i] = i - 1) this is the rule of vc_accept.
+ */
+VC_API vc_status vc_tree_accept(const int32_t *parent, const int32_t *tokens, const int32_t *verified,
+                                int32_t batch, int32_t n_q, int32_t *accept_len, int32_t *path, int32_t *emitted,
+                                vc_stream_t stream);
+
+/*
+ * vc_tree_commit -- keep the accepted path in KV_full: for j = 1 ..
+ * accept_len[b] the K and V of position base + path[b][j] move to base + j
+ * (in place, in every layer), after which positions up to base + accept_len[b]
+ * hold what a chain would have left there; later ones are void.  The caller
+ * then shortens seq_lens[b] to base + accept_len[b] + 1.
+ *  layers    host array of n_layers caches, bits == 16, that share format,
+ *            batch, max_blocks, num_pages, block_table and seq_lens (still
+ *            the length with the tree); each has pools of its own, on
+ *            16-byte boundaries (a pool given twice is refused).
+ * A path that does not ascend strictly from 0 and stay below n_q, a length
+ * outside [-1, n_q - 1] or seq_lens[b] < n_q leave the request as it was, and
+ * a bad page that entry (VC_ERR_BAD_INDEX in dev_status).
+ */
+VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int32_t n_q, const int32_t *accept_len,
+                                const int32_t *path, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_token_logprobs -- log probabilities of given tokens, the entropy and the
+ * most probable alternatives of each row of logits, p = softmax(x / tau):
+ *   y_v = (x_v - max x) / tau,  S = sum_v exp(y_v)
+ *   log p_v = y_v - log S,  entropy = log S - sum_v y_v exp(y_v) / S
+ *  logits        device, dtype VC_F32, VC_BF16 or VC_F16: row r at logits + r
+ *                * row_stride values, vocab of them (row_stride >= vocab)
+ *  ids           device int32 [rows][n_ids], n_ids >= 0: the tokens asked for.
+ *                -1 is no token (log probability 0); any other id outside [0,
+ *                vocab) gets 0 too and is reported (VC_ERR_BAD_INDEX)
+ *  temperature   tau > 0
+ *  logprobs      device fp32 [rows][n_ids]
+ *  entropy       device fp32 [rows], or NULL
+ *  top_ids       device int32 [rows][top_k], 0 <= top_k <= 64: the ids of the
+ *                largest logits in falling order, equal logits by lower id.
+ *                Logits of -infinity are not listed: -1 fills the rest
+ *  top_logprobs  device fp32 [rows][top_k], -infinity beside a -1
+ *  workspace     vc_token_logprobs_workspace_bytes(rows, vocab, top_k) bytes,
+ *                8-byte aligned
+ * Logits of -infinity (tokens ruled out) have probability 0 and add nothing
+ * to the entropy.  A row of nothing else gives -infinity (given tokens), 0
+ * (entropy) and an empty list.  A row that holds NaN or +infinity has no
+ * distribution: NaN everywhere, -1 for every alternative.  Sums are fp32; S is
+ * kept as the maxima's count plus the rest, so a row that is all but certain
+ * keeps its digits.
+ */
+VC_API size_t vc_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top_k);
+VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int32_t vocab,
+                                   int64_t row_stride, const int32_t *ids, int32_t n_ids, float temperature,
+                                   int32_t top_k, float *logprobs, float *entropy, int32_t *top_ids,
+                                   float *top_logprobs, void *workspace, size_t workspace_bytes,
+                                   int32_t *dev_status, vc_stream_t stream);
 
 /*
  * vc_debug_set_wait_fault -- fault injection for tests of the bounded device

@@ -16,6 +16,12 @@ staggering scheduler (``stagger_plan`` / ``stagger_simulate`` /
 ``stagger_horizon``, host code in the library; engine in ``stagger.py``) and
 the paced copy of an emulated slow link (``link_clock`` /
 ``stage_paced_async``; remote-prefix engine in ``remote.py``).
+
+Trees of drafts: ``rotary_kv_write`` (rotary positions in general form, K / V
+written at slots of their own), ``tree_plan`` (masks and positions),
+``tree_attn`` (the tree over KV_full), ``tree_accept`` / ``tree_commit`` (the
+greedy walk, the accepted path kept) and ``token_logprobs`` (log
+probabilities, entropy and the alternatives a tree is drawn from).
 """
 from __future__ import annotations
 
@@ -42,6 +48,12 @@ class PagedKVStruct(C.Structure):
     _fields_ = [("k_pages", C.c_void_p), ("v_pages", C.c_void_p), ("num_pages", C.c_int64),
                 ("block_table", C.c_void_p), ("seq_lens", C.c_void_p), ("batch", C.c_int32),
                 ("max_blocks", C.c_int32), ("fmt", KVFormat)]
+
+
+class RotaryStruct(C.Structure):
+    _fields_ = [("theta", C.c_float), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("factor", C.c_float),
+                ("original_len", C.c_int32), ("low_turns", C.c_float), ("high_turns", C.c_float),
+                ("amplitude", C.c_float)]
 
 
 class StaggerModel(C.Structure):
@@ -92,6 +104,17 @@ _SIG = {
     "vc_swiglu": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P]),
     "vc_rope_kv_write": (C.c_int, [_P, C.c_int32, _P, _P, C.c_int32, C.c_float, _P, C.POINTER(PagedKVStruct), _P,
                                    _P]),
+    "vc_rotary_kv_write": (C.c_int, [_P, C.c_int32, C.c_int64, C.c_int32, _P, _P, _P, C.c_int32,
+                                     C.POINTER(RotaryStruct), _P, C.POINTER(PagedKVStruct), _P, _P]),
+    "vc_tree_plan": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P, _P, _P, _P]),
+    "vc_tree_workspace_bytes": (C.c_size_t, [C.POINTER(PagedKVStruct), C.c_int32, C.c_int32, C.c_int32]),
+    "vc_tree_attn": (C.c_int, [_P, C.c_int32, C.c_int32, C.POINTER(PagedKVStruct), _P, C.c_float, _P, C.c_int32,
+                               C.c_int32, _P, C.c_size_t, _P, _P]),
+    "vc_tree_accept": (C.c_int, [_P, _P, _P, C.c_int32, C.c_int32, _P, _P, _P, _P]),
+    "vc_tree_commit": (C.c_int, [C.POINTER(PagedKVStruct), C.c_int32, C.c_int32, _P, _P, _P, _P]),
+    "vc_token_logprobs_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32]),
+    "vc_token_logprobs": (C.c_int, [_P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, _P, C.c_int32, C.c_float,
+                                    C.c_int32, _P, _P, _P, _P, _P, C.c_size_t, _P, _P]),
     "vc_draft_attn_static": (C.c_int, [_P, C.c_int32, C.POINTER(PagedKVStruct), C.c_float, _P, C.c_int32, _P, _P]),
     "vc_static_scratch_bytes": (C.c_size_t, []),
     "vc_stagger_plan": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P]),
@@ -430,6 +453,185 @@ def stagger_horizon(stage_bytes, draft_ns, verify_ns, link_bytes_per_ns: float, 
     _check(_lib.vc_stagger_horizon(C.byref(m.s), int(x_lo), int(x_hi), int(n_cycles), C.byref(x), _np_ptr(ph),
                                    C.byref(r)), "vc_stagger_horizon")
     return int(x.value), ph[:len(m.sb)], _result(r)
+
+
+# ---------------------------------------------------------------------------
+# a round that drafts a tree
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+
+
+def _need(name: str, t, dtype, shape):
+    """A contiguous tensor of this type and shape on the current device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
+    _here(name, t)
+
+
+def _here(name: str, t):
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device" % name)
+
+
+def _status(status):
+    if status is not None:
+        _need("status", status, _I32, (1,))
+    return _ptr(status)
+
+
+def _cache(full: PagedKV):
+    """The struct of a cache whose four tensors are on the current device."""
+    for name in ("k_pages", "v_pages", "block_table", "seq_lens"):
+        _here(name, getattr(full, name))
+    if full.seq_lens.shape != full.block_table.shape[:1] or full.v_pages.shape[0] != full.k_pages.shape[0]:
+        raise ValueError("block_table, seq_lens and the page pools disagree in size")
+    return full.struct()
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """Rotary positions (vc_rotary in include/vc.h): base theta, the first
+    rot_dim channels of a head, half or interleaved pairs, and frequencies
+    stretched by factor (all of them, or by how often a pair turns within
+    original_len)."""
+    theta: float
+    rot_dim: int
+    interleaved: bool = False
+    factor: float = 1.0
+    original_len: int = 0
+    low_turns: float = 0.0
+    high_turns: float = 0.0
+    amplitude: float = 1.0
+
+    def struct(self) -> RotaryStruct:
+        return RotaryStruct(self.theta, self.rot_dim, int(self.interleaved), self.factor, self.original_len,
+                            self.low_turns, self.high_turns, self.amplitude)
+
+
+def rotary_kv_write(qkv, row_req, row_pos, num_q_heads: int, rotary: Rotary, q_out, full: PagedKV, row_slot=None,
+                    status=None, stream=None):
+    """vc_rotary_kv_write: rotate the rows' Q and K by row_pos, q to q_out
+    (bf16 [m][Hq][D]), K and V into `full` at row_slot (row_pos when None).
+    qkv: fp32 or bf16 [m][(Hq + 2 Hkv) D], rows may be strided."""
+    m, width = qkv.shape
+    hkv, d = full.num_kv_heads, full.head_dim
+    dt = _DTYPES.get(qkv.dtype, -1)
+    if width != (num_q_heads + 2 * hkv) * d or (width > 1 and qkv.stride(1) != 1):
+        raise ValueError("qkv must be [m][(Hq + 2 Hkv) head_dim] with contiguous rows")
+    _here("qkv", qkv)
+    _need("row_req", row_req, _I32, (m,))
+    _need("row_pos", row_pos, _I32, (m,))
+    if row_slot is not None:
+        _need("row_slot", row_slot, _I32, (m,))
+    _need("q_out", q_out, _BF16, (m, num_q_heads, d))
+    fs, rs = _cache(full), rotary.struct()
+    _check(_lib.vc_rotary_kv_write(_ptr(qkv), dt, qkv.stride(0) if m > 1 else width, m, _ptr(row_req), _ptr(row_pos),
+                                   _ptr(row_slot), int(num_q_heads), C.byref(rs), _ptr(q_out), C.byref(fs),
+                                   _status(status), _stream(stream)), "vc_rotary_kv_write")
+
+
+def tree_plan(parent, seq_lens, mask, position, status=None, stream=None):
+    """vc_tree_plan: parent int32 [B][n_q] -> mask int64 [B][n_q] (the node
+    and its ancestors, one bit each) and position int32 [B][n_q]."""
+    b, n_q = parent.shape
+    _need("parent", parent, _I32, (b, n_q))
+    _need("seq_lens", seq_lens, _I32, (b,))
+    _need("mask", mask, _I64, (b, n_q))
+    _need("position", position, _I32, (b, n_q))
+    _check(_lib.vc_tree_plan(_ptr(parent), b, n_q, _ptr(seq_lens), _ptr(mask), _ptr(position), _status(status),
+                             _stream(stream)), "vc_tree_plan")
+
+
+def tree_workspace_bytes(full: PagedKV, n_q: int, num_q_heads: int, max_seq_len: int) -> int:
+    fs = full.struct()
+    return int(_lib.vc_tree_workspace_bytes(C.byref(fs), n_q, num_q_heads, int(max_seq_len)))
+
+
+def tree_attn(q, full: PagedKV, mask, softmax_scale: float, out, max_seq_len: int, workspace, status=None,
+              stream=None):
+    """vc_tree_attn: q bf16 [B][n_q][Hq][D] over KV_full, the last n_q entries
+    of which are a tree; out fp32 or bf16 of the same shape."""
+    b, n_q, hq, d = q.shape
+    if b != full.batch or d != full.head_dim:
+        raise ValueError("q must be [batch][n_q][num_q_heads][head_dim] of the cache")
+    _need("q", q, _BF16, q.shape)
+    _need("mask", mask, _I64, (b, n_q))
+    _need("out", out, out.dtype, q.shape)
+    _here("workspace", workspace)
+    fs = _cache(full)
+    _check(_lib.vc_tree_attn(_ptr(q), n_q, hq, C.byref(fs), _ptr(mask), float(softmax_scale), _ptr(out),
+                             _DTYPES.get(out.dtype, -1), int(max_seq_len), _ptr(workspace),
+                             workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
+           "vc_tree_attn")
+
+
+def tree_accept(parent, tokens, verified, accept_len, path, emitted, stream=None):
+    """vc_tree_accept: the greedy walk; all int32 [B][n_q], accept_len [B]."""
+    b, n_q = parent.shape
+    for name, t in (("parent", parent), ("tokens", tokens), ("verified", verified), ("path", path),
+                    ("emitted", emitted)):
+        _need(name, t, _I32, (b, n_q))
+    _need("accept_len", accept_len, _I32, (b,))
+    _check(_lib.vc_tree_accept(_ptr(parent), _ptr(tokens), _ptr(verified), b, n_q, _ptr(accept_len), _ptr(path),
+                               _ptr(emitted), _stream(stream)), "vc_tree_accept")
+
+
+class KVLayers:
+    """The caches of a model's layers as vc_tree_commit takes them (they share
+    block table, lengths and format); built once, kept by the caller."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        self.structs = (PagedKVStruct * len(self.caches))(*[_cache(c) for c in self.caches])
+
+    def __len__(self):
+        return len(self.caches)
+
+
+def tree_commit(layers: KVLayers, accept_len, path, status=None, stream=None):
+    """vc_tree_commit: move the accepted path's K / V to where a chain would
+    have put them, in every layer."""
+    b, n_q = path.shape
+    if len(layers) and layers.caches[0].batch != b:
+        raise ValueError("path must be [batch][n_q] of the caches")
+    _need("accept_len", accept_len, _I32, (b,))
+    _need("path", path, _I32, (b, n_q))
+    _check(_lib.vc_tree_commit(layers.structs, len(layers), n_q, _ptr(accept_len), _ptr(path), _status(status),
+                               _stream(stream)), "vc_tree_commit")
+
+
+def token_logprobs_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:
+    return int(_lib.vc_token_logprobs_workspace_bytes(int(rows), int(vocab), int(top_k)))
+
+
+def token_logprobs(logits, ids, logprobs, workspace, temperature: float = 1.0, entropy=None, top_ids=None,
+                   top_logprobs=None, status=None, stream=None):
+    """vc_token_logprobs: logits fp32 / bf16 / fp16 [rows][vocab] (rows may be
+    strided), ids int32 [rows][n_ids] -> logprobs fp32 [rows][n_ids], entropy
+    fp32 [rows], the top_ids.shape[1] largest logits' ids (int32) and log
+    probabilities (fp32), best first."""
+    rows, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("the rows of logits must be contiguous")
+    _here("logits", logits)
+    n_ids = ids.shape[1]
+    _need("ids", ids, _I32, (rows, n_ids))
+    _need("logprobs", logprobs, _F32, (rows, n_ids))
+    if entropy is not None:
+        _need("entropy", entropy, _F32, (rows,))
+    k = 0
+    if top_ids is not None:
+        k = top_ids.shape[1]
+        _need("top_ids", top_ids, _I32, (rows, k))
+        _need("top_logprobs", top_logprobs, _F32, (rows, k))
+    _here("workspace", workspace)
+    _check(_lib.vc_token_logprobs(_ptr(logits), _DTYPES.get(logits.dtype, -1), rows, vocab,
+                                  logits.stride(0) if rows > 1 else vocab, _ptr(ids), n_ids, float(temperature), k,
+                                  _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
+           "vc_token_logprobs")
 
 
 # ---------------------------------------------------------------------------

@@ -42,16 +42,6 @@ WaitFault g_wait_fault;
 WaitFault wait_fault() { return g_wait_fault; }
 
 namespace {
-// The format and batch of a paged cache (all an empty batch needs).
-bool paged_fmt_ok(const vc_paged_kv *p) {
-    return p && p->batch >= 0 && p->fmt.num_kv_heads >= 1 && p->fmt.head_dim >= 32 && p->fmt.head_dim % 32 == 0 &&
-           p->fmt.head_dim <= VC_MAX_HEAD_DIM;
-}
-// ... and its pools, table and lengths, for a batch with requests.
-bool paged_ok(const vc_paged_kv *p) {
-    return paged_fmt_ok(p) && p->k_pages && p->v_pages && p->block_table && p->seq_lens && p->max_blocks >= 1 &&
-           p->num_pages >= 1;
-}
 bool bits_ok(int b) { return b == 2 || b == 3 || b == 4 || b == 16; }
 vc_status from_cuda(cudaError_t e) { return e == cudaSuccess ? VC_OK : VC_ERR_CUDA; }
 }  // namespace

@@ -1,0 +1,179 @@
+// vc_rotary_kv_write: rotary positions in general form, with the rotated K
+// and the V of each row written into KV_full.
+//
+//   (a, b) -> amplitude (a cos t - b sin t, b cos t + a sin t),  t = pos f_i
+//
+// The angle: f_i / 2pi turns per position is handed over as a binary
+// fraction of 64 bits, F_i (computed in double: off by at most 2^-55 turn);
+// pos * F_i modulo 2^64 is then the fraction of a turn to within pos * 2^-55
+// (2^-35 at a million).  In fp32 the product pos * f_i alone would be off by
+// 2^-25 pos radians (0.004 at 131072).
+#include <cmath>
+
+#include "vc_internal.cuh"
+
+namespace vc {
+namespace {
+
+constexpr int kMaxPairs = VC_MAX_HEAD_DIM / 2;
+
+struct RotArgs {
+    const void *qkv;
+    int64_t stride;  // values per row
+    const int32_t *req, *pos, *slot;
+    int m, hq, hkv, d, half, inter;
+    float amp;
+    uint16_t *q;
+    uint16_t *kp, *vp;
+    int64_t n_pages;
+    const int32_t *table;
+    int maxb, batch;
+    int32_t *status;
+    uint64_t turns[kMaxPairs];  // F_i
+};
+
+// cos and sin (times the amplitude) of pair i at a position.  The fraction of
+// a turn as a signed 32-bit number of 2^-32 turns, so the angle lies in
+// [-pi, pi], where the fast sine and cosine are off by at most 2^-21: the
+// result is rounded to bf16, whose half step is 2^-8 of the value.
+__device__ inline float2 cos_sin(uint64_t turns, int pos, float amp) {
+    const int32_t frac = (int32_t)((turns * (uint64_t)(uint32_t)pos) >> 32);
+    float s, c;
+    __sincosf((float)frac * 1.4629180792671596e-9f, &s, &c);  // 2 pi / 2^32
+    return make_float2(c * amp, s * amp);
+}
+
+// The cache slot a row writes: offset (in values) of kv head 0's row, or -1
+// for a row to be skipped (padding, or out of range, which is reported).
+__device__ inline int64_t row_base(const RotArgs &a, int r) {
+    const int b = a.req[r];
+    if (b == -1) return -1;
+    const int pos = a.pos[r], slot = a.slot ? a.slot[r] : pos;
+    int page = -1;
+    if (b >= 0 && b < a.batch && pos >= 0 && slot >= 0 && slot / kPage < a.maxb)
+        page = a.table[(int64_t)b * a.maxb + slot / kPage];
+    if (page < 0 || page >= a.n_pages) {
+        report(a.status, VC_ERR_BAD_INDEX);
+        return -1;
+    }
+    return ((int64_t)page * a.hkv * kPage + slot % kPage) * a.d;
+}
+
+__device__ inline float load1(const float *p) { return *p; }
+__device__ inline float load1(const uint16_t *p) { return bf16_bits_to_f32(*p); }
+__device__ inline uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+
+// One block per row, one thread per channel pair of a head.
+template <typename T>
+__global__ void __launch_bounds__(256) rotary_pairs_kernel(const __grid_constant__ RotArgs a) {
+    pdl_begin();
+    __shared__ float2 cs[kMaxPairs];
+    __shared__ int64_t base_s;
+    const int r = blockIdx.x;
+    if (threadIdx.x == 0) base_s = row_base(a, r);
+    __syncthreads();
+    const int64_t base = base_s;
+    if (base < 0) return;
+    const int pos = a.pos[r];
+    for (int i = threadIdx.x; i < a.half; i += blockDim.x) cs[i] = cos_sin(a.turns[i], pos, a.amp);
+    __syncthreads();
+    const T *x = reinterpret_cast<const T *>(a.qkv) + (int64_t)r * a.stride;
+    const int nh = a.hq + 2 * a.hkv, pairs = a.d / 2;
+    for (int e = threadIdx.x; e < nh * pairs; e += blockDim.x) {
+        const int h = e / pairs, i = e % pairs;
+        // pairs past the rotated ones: neighbouring channels, copied
+        const bool turn = i < a.half;
+        const int c0 = turn && !a.inter ? i : 2 * i, c1 = turn && !a.inter ? i + a.half : 2 * i + 1;
+        const float x0 = load1(x + h * a.d + c0), x1 = load1(x + h * a.d + c1);
+        float y0 = x0, y1 = x1;
+        if (turn && h < a.hq + a.hkv) {
+            y0 = x0 * cs[i].x - x1 * cs[i].y;
+            y1 = x1 * cs[i].x + x0 * cs[i].y;
+        }
+        uint16_t *dst;
+        if (h < a.hq)
+            dst = a.q + ((int64_t)r * a.hq + h) * a.d;
+        else if (h < a.hq + a.hkv)
+            dst = a.kp + base + (int64_t)(h - a.hq) * kPage * a.d;
+        else
+            dst = a.vp + base + (int64_t)(h - a.hq - a.hkv) * kPage * a.d;
+        dst[c0] = bf16_bits(y0);
+        dst[c1] = bf16_bits(y1);
+    }
+}
+
+// F_i of every pair, from 64-bit frequencies.
+void fill_turns(const vc_rotary &p, uint64_t *turns) {
+    constexpr double kTwoPi = 6.283185307179586476925;
+    const int half = p.rot_dim / 2;
+    const double step = half ? -std::log((double)p.theta) / half : 0.0;
+    for (int i = 0; i < half; ++i) {
+        double f = std::exp(step * i);
+        if (p.factor != 1.0f) {
+            double g = 0.0;
+            if (p.original_len > 0) {
+                g = (p.original_len * f / kTwoPi - p.low_turns) / ((double)p.high_turns - p.low_turns);
+                g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
+            }
+            f *= g + (1.0 - g) / p.factor;
+        }
+        turns[i] = (uint64_t)std::ldexp(f / kTwoPi, 64);  // f <= 1: below half a turn
+    }
+}
+
+bool rotary_ok(const vc_rotary *p, int d) {
+    if (!p || p->rot_dim < 0 || p->rot_dim % 2 || p->rot_dim > d) return false;
+    if (!std::isfinite(p->theta) || p->theta < 1.0f || !std::isfinite(p->factor) || p->factor < 1.0f) return false;
+    if (p->original_len < 0 || !std::isfinite(p->amplitude)) return false;
+    if (p->original_len > 0 && p->factor != 1.0f &&
+        !(std::isfinite(p->low_turns) && std::isfinite(p->high_turns) && p->low_turns < p->high_turns))
+        return false;
+    return true;
+}
+
+}  // namespace
+}  // namespace vc
+
+using namespace vc;
+
+extern "C" vc_status vc_rotary_kv_write(const void *qkv, int32_t qkv_dtype, int64_t row_stride, int32_t m,
+                                        const int32_t *row_req, const int32_t *row_pos, const int32_t *row_slot,
+                                        int32_t num_q_heads, const vc_rotary *rotary, void *q_out,
+                                        const vc_paged_kv *full, int32_t *dev_status, vc_stream_t stream) {
+    if (!paged_fmt_ok(full) || m < 0 || num_q_heads < 1 || !rotary_ok(rotary, full->fmt.head_dim) ||
+        row_stride < ((int64_t)num_q_heads + 2 * (int64_t)full->fmt.num_kv_heads) * full->fmt.head_dim)
+        return VC_ERR_INVALID_ARG;
+    if (full->fmt.bits != 16 || (qkv_dtype != VC_F32 && qkv_dtype != VC_BF16)) return VC_ERR_UNSUPPORTED;
+    if (m == 0 || full->batch == 0) return VC_OK;
+    if (!qkv || !row_req || !row_pos || !q_out || !full->k_pages || !full->v_pages || !full->block_table ||
+        full->max_blocks < 1 || full->num_pages < 1)
+        return VC_ERR_INVALID_ARG;
+    RotArgs a;
+    a.qkv = qkv;
+    a.stride = row_stride;
+    a.req = row_req;
+    a.pos = row_pos;
+    a.slot = row_slot;
+    a.m = m;
+    a.hq = num_q_heads;
+    a.hkv = full->fmt.num_kv_heads;
+    a.d = full->fmt.head_dim;
+    a.half = rotary->rot_dim / 2;
+    a.inter = rotary->interleaved != 0;
+    a.amp = rotary->amplitude;
+    a.q = (uint16_t *)q_out;
+    a.kp = (uint16_t *)full->k_pages;
+    a.vp = (uint16_t *)full->v_pages;
+    a.n_pages = full->num_pages;
+    a.table = full->block_table;
+    a.maxb = full->max_blocks;
+    a.batch = full->batch;
+    a.status = dev_status;
+    fill_turns(*rotary, a.turns);
+    cudaError_t e;
+    if (qkv_dtype == VC_F32)
+        e = launch_pdl(rotary_pairs_kernel<float>, m, 256, 0, (cudaStream_t)stream, a);
+    else
+        e = launch_pdl(rotary_pairs_kernel<uint16_t>, m, 256, 0, (cudaStream_t)stream, a);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? VC_OK : VC_ERR_CUDA;
+}

@@ -26,6 +26,20 @@ __host__ __device__ inline int head_block_bytes(int bits, int d) {
 // Byte size of one token slot's packed codes.
 __host__ __device__ inline int code_row_bytes(int bits, int d) { return d * bits / 8; }
 
+// The format and batch of a paged cache (all an empty batch needs).
+inline bool paged_fmt_ok(const vc_paged_kv *p) {
+    return p && p->batch >= 0 && p->fmt.num_kv_heads >= 1 && p->fmt.head_dim >= 32 && p->fmt.head_dim % 32 == 0 &&
+           p->fmt.head_dim <= VC_MAX_HEAD_DIM;
+}
+// ... and its pools, table and lengths, for a batch with requests.
+inline bool paged_ok(const vc_paged_kv *p) {
+    return paged_fmt_ok(p) && p->k_pages && p->v_pages && p->block_table && p->seq_lens && p->max_blocks >= 1 &&
+           p->num_pages >= 1;
+}
+
+// Bytes of one value of a vc_dtype; 0 for another number.
+inline int dtype_bytes(int t) { return t == VC_F32 ? 4 : (t == VC_BF16 || t == VC_F16) ? 2 : 0; }
+
 // First error wins; the caller zeroes the word before the launch.
 __device__ inline void report(int32_t *st, int code) {
     if (st) atomicCAS(st, 0, code);
