@@ -63,6 +63,8 @@ EncodeTiled encoder() {
     return fn;
 }
 
+}  // namespace
+
 // A page pool seen by the TMA unit: rows = pages * kv heads * 16 tokens,
 // D bf16 channels each; boxes of 16 rows x 64 channels, 128-byte swizzle.
 bool encode_pool(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d) {
@@ -76,8 +78,6 @@ bool encode_pool(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-}  // namespace
 
 int verify_splits(int max_seq_len) { return max(1, ceil_div(ceil_div(max_seq_len, kPage), vtc::kSplitPages)); }
 
