@@ -628,7 +628,7 @@ VC_API vc_status vc_tree_plan(const int32_t *parent, int32_t batch, int32_t n_q,
  *              or VC_BF16 (the probabilities enter the second product in bf16
  *              either way, as in vc_verify_attn)
  * Limits and the other arguments are vc_verify_attn's; softmax_scale > 0; the
- * pools lie on 16-byte boundaries, q and out too.  A request with seq_lens[b] < n_q, or of
+ * pools, q and out lie on 16-byte boundaries, the workspace on a 32-byte one.  A request with seq_lens[b] < n_q, or of
  * more than max_seq_len, gets VC_ERR_BAD_INDEX in dev_status and zeros.
  * Entries of the tree that a node does not attend to do not touch its result,
  * whatever they hold (infinities and NaN included); a node that attends to an

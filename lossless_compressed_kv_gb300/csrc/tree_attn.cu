@@ -18,28 +18,41 @@ __global__ void __launch_bounds__(tree::Cfg<D, QT>::THREADS, tree::Cfg<D, QT>::M
 }
 
 template <int D, int QT>
-__global__ void __launch_bounds__(128) tree_join_kernel(const __grid_constant__ tree::Args a) {
+__global__ void __launch_bounds__(tree::kJoinRows * 32) tree_join_kernel(const __grid_constant__ tree::Args a) {
     pdl_begin();
     tree::tree_join_block<D, QT>(a);
 }
 
-// How a call is laid out over the GPU.
+// How a launch is laid out over the GPU; a call takes one, or two for three
+// tiles of rows (see tree_tc.cuh).
 struct Plan {
-    int tiles, lanes, groups, rows;  // rows: of a CTA
+    int tile0, tiles, lanes, groups, rows;  // rows: of a CTA
     int64_t slots() const { return (int64_t)groups * lanes * 2 * rows; }  // partial rows in the workspace
 };
-Plan plan_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len) {
-    Plan p;
-    p.tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows);
-    const bool one = p.tiles == 1;
-    p.lanes = p.tiles == 3 ? 3 : p.tiles == 4 ? 2 : 1;
-    p.rows = one ? tree::kTileRows : 2 * tree::kTileRows;
-    const int most = (one ? 2 * tree::kSMs : tree::kSMs) / p.lanes, bk = one ? 64 : 128;
-    const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, bk);
-    p.groups = (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
-    return p;
+int plans_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len, Plan (&p)[2]) {
+    const int tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows);
+    auto plan = [&](int t0, int t1) {
+        const bool one = t1 - t0 == 1;
+        const int lanes = t1 - t0 == 4 ? 2 : 1, most = (one ? 2 * tree::kSMs : tree::kSMs) / lanes;
+        const int bk = one ? tree::Cfg<128, 1>::BK : tree::Cfg<128, 2>::BK;
+        const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, bk);
+        return Plan{t0, t1, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most),
+                    (one ? 1 : 2) * tree::kTileRows};
+    };
+    if (tiles == 3) {
+        p[0] = plan(0, 2);
+        p[1] = plan(2, 3);
+        return 2;
+    }
+    p[0] = plan(0, tiles);
+    return 1;
 }
-size_t workspace_of(const Plan &p, int d) { return (size_t)p.slots() * (d + 2) * sizeof(float); }
+// (the launches of a call follow one another: they share the workspace)
+size_t workspace_of(const Plan *p, int n, int d) {
+    int64_t most = 0;
+    for (int i = 0; i < n; ++i) most = p[i].slots() > most ? p[i].slots() : most;
+    return (size_t)most * (d + 2) * sizeof(float);
+}
 
 template <int D, int QT>
 cudaError_t launch(const tree::Args &a, cudaStream_t st) {
@@ -48,8 +61,9 @@ cudaError_t launch(const tree::Args &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_kernel<D, QT>, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
     if (e != cudaSuccess) return e;
-    const dim3 grid(a.batch * a.hkv, ceil_div(a.n_q * a.grp, tree::kJoinRows));
-    e = launch_pdl(tree_join_kernel<D, QT>, grid, 128, 0, st, a);
+    const int rows = min(a.n_q * a.grp, a.tiles * tree::kTileRows) - a.tile0 * tree::kTileRows;
+    const dim3 grid(a.batch * a.hkv, ceil_div(rows, tree::kJoinRows));
+    e = launch_pdl(tree_join_kernel<D, QT>, grid, tree::kJoinRows * 32, 0, st, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -63,7 +77,8 @@ extern "C" {
 size_t vc_tree_workspace_bytes(const vc_paged_kv *full, int32_t n_q, int32_t num_q_heads, int32_t max_seq_len) {
     if (!full || full->batch < 0 || max_seq_len < 0 || n_q < 1 || !verify_supported(full->fmt, num_q_heads, n_q))
         return 0;
-    return workspace_of(plan_of(*full, n_q, num_q_heads, max_seq_len), full->fmt.head_dim);
+    Plan p[2];
+    return workspace_of(p, plans_of(*full, n_q, num_q_heads, max_seq_len, p), full->fmt.head_dim);
 }
 
 vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_paged_kv *full,
@@ -75,11 +90,11 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
         return VC_ERR_UNSUPPORTED;
     if (full->batch == 0) return VC_OK;
     if (!q || !mask || !out || !paged_ok(full) || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) ||
-        ((uintptr_t)full->k_pages & 15) || ((uintptr_t)full->v_pages & 15) || ((uintptr_t)workspace & 15))
+        ((uintptr_t)full->k_pages & 15) || ((uintptr_t)full->v_pages & 15) || ((uintptr_t)workspace & 31))
         return VC_ERR_INVALID_ARG;
-    const Plan p = plan_of(*full, n_q, num_q_heads, max_seq_len);
-    const int d = full->fmt.head_dim;
-    if (!workspace || workspace_bytes < workspace_of(p, d)) return VC_ERR_WORKSPACE;
+    Plan p[2];
+    const int n = plans_of(*full, n_q, num_q_heads, max_seq_len, p), d = full->fmt.head_dim;
+    if (!workspace || workspace_bytes < workspace_of(p, n, d)) return VC_ERR_WORKSPACE;
     tree::Args a;
     a.q = (const uint16_t *)q;
     a.n_pages = full->num_pages;
@@ -93,12 +108,8 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
     a.hkv = full->fmt.num_kv_heads;
     a.grp = num_q_heads / a.hkv;
     a.max_len = max_seq_len;
-    a.lanes = p.lanes;
-    a.tiles = p.tiles;
-    a.groups = p.groups;
     a.scale_log2 = softmax_scale * 1.4426950408889634f;
     a.ws_o = (float *)workspace;
-    a.ws_ml = a.ws_o + (size_t)p.slots() * d;
     a.out = out;
     a.out_bf16 = out_dtype == VC_BF16;
     a.status = dev_status;
@@ -108,9 +119,18 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
         !encode_pool(&a.vmap, full->v_pages, full->num_pages, a.hkv, d))
         return VC_ERR_CUDA;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = d == 64 ? (p.tiles == 1 ? launch<64, 1>(a, st) : launch<64, 2>(a, st))
-                                  : (p.tiles == 1 ? launch<128, 1>(a, st) : launch<128, 2>(a, st));
-    return e == cudaSuccess ? VC_OK : VC_ERR_CUDA;
+    for (int i = 0; i < n; ++i) {
+        a.tile0 = p[i].tile0;
+        a.tiles = p[i].tiles;
+        a.lanes = p[i].lanes;
+        a.groups = p[i].groups;
+        a.ws_ml = a.ws_o + (size_t)p[i].slots() * d;
+        const bool one = p[i].rows == tree::kTileRows;
+        const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, st) : launch<64, 2>(a, st))
+                                      : (one ? launch<128, 1>(a, st) : launch<128, 2>(a, st));
+        if (e != cudaSuccess) return VC_ERR_CUDA;
+    }
+    return VC_OK;
 }
 
 }  // extern "C"

@@ -17,11 +17,10 @@
 //
 // Tiles.  Rows are cut into tiles of 128 (one MMA's M).  One tile: CTAs of
 // one tile, two to an SM, which overlap each other's S / softmax / P V chain.
-// More: CTAs of two tiles, one to an SM, whose tiles take turns on the tensor
+// Two: CTAs of two tiles, one to an SM, whose tiles take turns on the tensor
 // core.  Four tiles: groups of two CTAs, two tiles each, on the same range in
-// step, so the second CTA finds K and V in L2.  Three tiles: groups of three
-// CTAs -- two share tiles 0 and 1 and take every other block, the third has
-// tile 2 and all blocks -- which keeps the three in step.
+// step, so the second CTA finds K and V in L2.  Three tiles: a launch of two
+// and one of one.
 //
 // A CTA: a producer warp that fills a ring of K and V blocks by TMA (one
 // 16-row x 64-channel box per page and 128-byte column), one thread that
@@ -56,8 +55,8 @@ struct Args {
     const int32_t *table, *lens;
     const unsigned long long *mask;  // [B][n_q]
     int batch, maxb, n_q, hq, hkv, grp, max_len;
-    int lanes;   // CTAs per group
-    int tiles;   // 128-row tiles of a unit
+    int lanes;        // CTAs per group
+    int tile0, tiles; // 128-row tiles [tile0, tiles) of a unit in this launch
     int groups;  // G
     float scale_log2;
     float *ws_o;   // [CTA][2][rows of a CTA][D]
@@ -71,25 +70,36 @@ struct Args {
 
 template <int D, int QT>
 struct Cfg {
-    static constexpr int NC = D / 64;           // 128-byte columns of a row
+    static constexpr int NC = D / 64;        // 128-byte columns of a row
+    // Keys per block.  One S instruction (M 128, N = BK, K 16) takes 64 cycles
+    // to fetch its A operand from TMEM whatever N is, and the math of N = 128
+    // takes 68: two-tile CTAs, which the tensor core bounds, take 128 keys and
+    // keep Q in shared memory; one-tile CTAs, which memory bounds, take 64.
     static constexpr int BK = QT == 1 ? 64 : 128;
-    static constexpr bool QTM = QT == 1;        // Q in TMEM beside S and O (else in shared memory)
+    static constexpr int PG = BK / kPage;    // pages of a block
+    static constexpr int SLOT = BK * D * 2;  // one block of K or of V
+    static constexpr bool QTM = QT == 1;     // Q in TMEM
     static constexpr int QTILE = kTileRows * D * 2;
-    static constexpr int SLOT = BK * D * 2;     // one block of K or of V
     static constexpr int OFF_KV = QTM ? 0 : QT * QTILE;
-    static constexpr int FIT = ((QT == 1 ? 100 : 225) * 1024 - OFF_KV) / SLOT;
-    static constexpr int SLOTS = FIT < 12 ? FIT : 12;
-    static_assert(SLOTS >= 4 && SLOTS / 2 + 2 <= kBadRing, "ring depth");
+    static constexpr int FIT = ((QT == 1 ? 110 : 224) * 1024 - OFF_KV) / SLOT;
+    static constexpr int SLOTS = FIT < 14 ? FIT : 14;
+    static_assert(SLOTS >= 5 && SLOTS / 2 + 2 <= kBadRing, "ring depth");
     static constexpr int OFF_BAR = OFF_KV + SLOTS * SLOT;
     static constexpr int NBAR = 4 * QT + 2 * SLOTS + 1;  // q, s, p, o per tile; full, empty; tail
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 64 * 4 + 1024;
+    static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 64 * 4;
+    static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "shared memory of the CTAs an SM holds");
+    // TMEM columns: S (then P) and O of each tile, Q (bf16 pairs)
     static constexpr int O_COL0 = QT * BK;
     static constexpr int Q_COL0 = O_COL0 + QT * D;
     static constexpr int TMEM_USED = Q_COL0 + (QTM ? D / 2 : 0);
     static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
     static_assert(TMEM_USED <= (QT == 1 ? 256 : 512), "TMEM columns");
-    static constexpr int WARPS = QT * 4 + 2;
+    static constexpr int SM_WARPS = QT * 4;  // softmax warps
+    // two-tile CTAs: the third warpgroup (producer, MMA issue, two idle warps)
+    // gives registers up for the softmax warps, which hold 128 scores each
+    static constexpr int WARPS = QT == 1 ? 6 : 12;
+    static constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;  // 2 x 128 x 216 + 128 x 72 = 384 x 168
     static constexpr int THREADS = WARPS * 32;
     static constexpr int MIN_CTAS = QT == 1 ? 2 : 1;
     static constexpr int ROWS = QT * kTileRows;
@@ -136,18 +146,6 @@ __device__ inline Sums sum_blocks(const Args &a, int64_t *sh, int tid, int nthre
 // The range of group g among G: blocks [g T / G, (g + 1) T / G) of T.
 __host__ __device__ inline int64_t range_start(int64_t total, int g, int groups) { return total * g / groups; }
 
-// Which blocks of a segment [b0, b0 + n) a CTA of lane `lane` takes: every
-// `step`-th from `first`, `count` of them.  whole: the segment is the unit.
-struct Share {
-    int first, step, count;
-};
-__device__ inline Share share_of(int lanes, int lane, int64_t unit, int b0, int n, bool whole) {
-    if (lanes < 3 || lane == 2) return {b0, 1, n};
-    if (whole) return {b0, 1, (int)(unit & 1) == lane ? n : 0};
-    const int first = b0 + ((b0 ^ lane) & 1), end = b0 + n;
-    return {first, 2, first < end ? (end - first + 1) / 2 : 0};
-}
-
 // A group's walk through its range.
 template <int BK>
 struct Walk {
@@ -155,8 +153,7 @@ struct Walk {
     int64_t left;
     bool first;
     // the current segment
-    int seg_b, seg_kvh, seg_len, seg_blk;
-    Share sh;
+    int seg_b, seg_kvh, seg_len, seg_blk, seg_n;
     bool whole, at_start;
 
     __device__ void begin(const Args &a, int b_, int kvh_, int blk_, int64_t left_) {
@@ -170,65 +167,81 @@ struct Walk {
             len = a.lens[b];
         }
     }
-    // The next segment in which this CTA has blocks.
-    __device__ bool next(const Args &a, int lane) {
-        while (left > 0) {
-            while (blk >= nblk) {  // the next unit that has blocks
-                blk = 0;
-                if (++kvh == a.hkv) {
-                    kvh = 0;
-                    ++b;
-                    nblk = blocks_of<BK>(a, b);
-                    len = a.lens[b];
-                }
+    // The next segment.
+    __device__ bool next(const Args &a) {
+        if (left <= 0) return false;
+        while (blk >= nblk) {  // the next unit that has blocks
+            blk = 0;
+            if (++kvh == a.hkv) {
+                kvh = 0;
+                ++b;
+                nblk = blocks_of<BK>(a, b);
+                len = a.lens[b];
             }
-            const int n = (int)min((int64_t)(nblk - blk), left);
-            whole = n == nblk;
-            at_start = first;
-            sh = share_of(a.lanes, lane, (int64_t)b * a.hkv + kvh, blk, n, whole);
-            seg_b = b;
-            seg_kvh = kvh;
-            seg_len = len;
-            seg_blk = blk;
-            first = false;
-            left -= n;
-            blk += n;
-            if (sh.count > 0) return true;
         }
-        return false;
+        seg_n = (int)min((int64_t)(nblk - blk), left);
+        whole = seg_n == nblk;
+        at_start = first;
+        seg_b = b;
+        seg_kvh = kvh;
+        seg_len = len;
+        seg_blk = blk;
+        first = false;
+        left -= seg_n;
+        blk += seg_n;
+        return true;
     }
 };
 
-// 128 consecutive columns of this thread's lane: one load, one wait
-__device__ inline void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-    uint32_t r[128];
-#define VC_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+// tcgen05.mma and commit by one elected thread of a warp that runs in step.
+__device__ inline void umma(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
-        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63,"
-        "%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
-        "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95,"
-        "%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
-        "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127"
-        "}, [%128];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : VC_R8(0), VC_R8(8), VC_R8(16), VC_R8(24), VC_R8(32), VC_R8(40), VC_R8(48), VC_R8(56), VC_R8(64), VC_R8(72),
-          VC_R8(80), VC_R8(88), VC_R8(96), VC_R8(104), VC_R8(112), VC_R8(120)
-        : "r"(taddr)
-        : "memory");
-#undef VC_R8
-#pragma unroll
-    for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc));
 }
+__device__ inline void umma_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(b), "r"(idesc), "r"(acc));
+}
+__device__ inline void umma_commit(uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// Two values in one packed instruction, each rounded as its scalar form.
+__device__ inline void fma2(float &d0, float &d1, float a0, float a1, float b, float c) {
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+        "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+        : "=f"(d0), "=f"(d1)
+        : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ inline void add2(float &d0, float &d1, float a0, float a1) {
+    asm("{\n\t.reg .b64 ra, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rd, {%0, %1};\n\t"
+        "add.rn.f32x2 rd, rd, ra;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
+}
+__device__ inline float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// max of N values: four chains of three-input maxima (exact in any order)
 template <int N>
-__device__ inline void tmem_ld_block(uint32_t taddr, float (&v)[N]) {
-    if constexpr (N == 128)
-        tmem_ld128(taddr, v);
-    else
-        vtc::tmem_ld_row<N>(taddr, v);
+__device__ inline float max_of(const float (&v)[N]) {
+    float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 4; i < N; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = i + 4 + k < N ? max3(m[k], v[i + k], v[i + 4 + k]) : fmaxf(m[k], v[i + k]);
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
 // 16 bytes of bf16 without their infinities and NaN (set to 0); whether there were any.
@@ -258,6 +271,11 @@ __device__ inline unsigned long long seen_bits(unsigned long long mask, int key0
 }
 
 // One row's result: the final value of a finished unit, in out's type.
+__device__ inline void store_ws8(float *dst, const float *v) {  // 32 bytes, one sector
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 template <int D>
 __device__ inline void store_out16(const Args &a, int64_t orow, int c0, const float (&v)[16], float f, bool zero) {
     float y[16];
@@ -276,12 +294,14 @@ __device__ inline void store_out16(const Args &a, int64_t orow, int c0, const fl
 }
 
 template <int D, int QT>
-__device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
+__device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     using C = Cfg<D, QT>;
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // 1024-byte aligned
+    constexpr int BK = C::BK, PG = C::PG;
+    if (smem_u32(smem) & 1023u) {  // (the swizzled tiles start on 1024-byte boundaries: the array is declared so)
+        if (threadIdx.x == 0) report(a.status, VC_ERR_UNSUPPORTED);
+        return;
+    }
     uint8_t *sq = smem;
-    uint8_t *skv = smem + C::OFF_KV;
     uint64_t *q_ready = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [QT]
     uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + QT, *o_done = p_ready + QT;
     uint64_t *full = o_done + QT, *empty = full + C::SLOTS, *tail = empty + C::SLOTS;
@@ -293,16 +313,16 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp_id = blockIdx.x / a.lanes, glane = blockIdx.x % a.lanes;
-    // this CTA's tiles: all of one tile; or 0, 1 | 2, 3; of three, lane 2 has the last alone
-    const int tile0 = QT == 1 ? 0 : a.lanes == 3 ? (glane == 2 ? 2 : 0) : 2 * glane;
-    const int nt = QT == 1 ? 1 : a.lanes == 3 && glane == 2 ? 1 : min(QT, a.tiles - tile0);
+    const int tile0 = a.tile0 + QT * glane, nt = min(QT, a.tiles - tile0);  // this CTA's tiles
+
+    uint8_t *skv = smem + C::OFF_KV;
 
     // ---- set-up ----
     if (tid == 0) {
         for (int t = 0; t < QT; ++t) {
-            mbar_init(&q_ready[t], kTileRows);
+            mbar_init(&q_ready[t], 4);
             mbar_init(&s_ready[t], 1);
-            mbar_init(&p_ready[t], kTileRows);
+            mbar_init(&p_ready[t], 4);
             mbar_init(&o_done[t], 1);
         }
         for (int i = 0; i < C::SLOTS; ++i) {
@@ -318,15 +338,15 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     vtc::tc_fence_before();
-    const Sums sm = sum_blocks<C::BK>(a, sums, tid, C::THREADS);  // (holds a __syncthreads)
+    const Sums sm = sum_blocks<BK>(a, sums, tid, C::THREADS);  // (holds a __syncthreads)
     const int64_t total = sm.total * a.hkv;
     const int64_t f0 = range_start(total, grp_id, a.groups), f1 = range_start(total, grp_id + 1, a.groups);
     if (f0 < f1 && f0 >= sm.before * a.hkv && f0 < (sm.before + sm.mine) * a.hkv) {
         int64_t rem = f0 - sm.before * a.hkv;
-        int b = sm.b0, n = blocks_of<C::BK>(a, b);
+        int b = sm.b0, n = blocks_of<BK>(a, b);
         while (rem >= (int64_t)n * a.hkv) {
             rem -= (int64_t)n * a.hkv;
-            n = blocks_of<C::BK>(a, ++b);
+            n = blocks_of<BK>(a, ++b);
         }
         where[0] = b;
         where[1] = (int)(rem / n);
@@ -335,24 +355,24 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
     __syncthreads();
     vtc::tc_fence_after();
     const uint32_t tmem = *tslot;
-    Walk<C::BK> w;
+    Walk<BK> w;
     w.begin(a, f0 < f1 ? where[0] : 0, f0 < f1 ? where[1] : 0, f0 < f1 ? where[2] : 0, f1 - f0);
 
-    constexpr uint32_t IQK = vtc::idesc_bf16(128, C::BK, false);
+    constexpr uint32_t IQK = vtc::idesc_bf16(128, BK, false);
     constexpr uint32_t IPV = vtc::idesc_bf16(128, D, true);
-    constexpr int PG = C::BK / kPage;  // pages of a block
     bool alive = true;
 
-    if (warp == QT * 4) {
+    if (warp == C::SM_WARPS) {
         // ================= producer =================
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         if (!a.skip_copies) {
             uint32_t seq = 0;   // copies into the ring so far
             int seg = 0;
             uint32_t tails = 0;
             // V blocks of the tree that are under way, oldest first
-            struct Pend { uint32_t seq; int key0, len, seg; } pend{};
+            struct Pend { int slot, key0, len, seg; } pend{};
             bool pending = false;
-            int64_t lost = -1;  // a tree block whose copy did not arrive in time
+            int lost = -1;  // slot of a tree block whose copy did not arrive in time
             // wait for the pending V block, clear what must not be read, hand it on
             auto flush = [&]() {
                 if (!pending) return;
@@ -360,16 +380,16 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 alive = __all_sync(0xffffffffu, mbar_wait(tail, tails & 1, a.status, a.wait_ns));
                 ++tails;
                 if (!alive) {
-                    lost = pend.seq;
+                    lost = pend.slot;
                     return;
                 }
-                const int slot = pend.seq % C::SLOTS, base = pend.len - a.n_q;
-                uint8_t *vt = skv + slot * C::SLOT;
+                const int base = pend.len - a.n_q;
+                uint8_t *vt = skv + pend.slot * C::SLOT;
                 unsigned long long found = 0;
                 const int r0 = max(0, base - pend.key0);
-                for (int e = lane; e < (C::BK - r0) * (D / 8); e += 32) {
+                for (int e = lane; e < (BK - r0) * (D / 8); e += 32) {
                     const int r = r0 + e / (D / 8), c = e % (D / 8);
-                    uint4 *p = reinterpret_cast<uint4 *>(vt + vtc::sw128(r, c, C::BK));
+                    uint4 *p = reinterpret_cast<uint4 *>(vt + vtc::sw128(r, c, BK));
                     const int node = pend.key0 + r - base;
                     if (node >= a.n_q) {
                         *p = make_uint4(0, 0, 0, 0);
@@ -384,9 +404,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 if (found) atomicOr(&bad[pend.seg % kBadRing], found);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
+                if (lane == 0) mbar_arrive(&full[pend.slot]);
             };
-            while (alive && w.next(a, glane)) {
+            while (alive && w.next(a)) {
                 const int32_t *trow = a.table + (int64_t)w.seg_b * a.maxb;
                 const int npages = ceil_div(w.seg_len, kPage);
                 if (lane == 0) bad[seg % kBadRing] = 0;
@@ -397,8 +417,8 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 auto load_ids = [&](int i0) {
                     const int i = i0 + lane / PG;
                     int id = 0;
-                    if (i < w.sh.count) {
-                        const int pidx = (w.sh.first + i * w.sh.step) * PG + lane % PG;
+                    if (i < w.seg_n) {
+                        const int pidx = (w.seg_blk + i) * PG + lane % PG;
                         if (pidx < npages) {
                             id = pidx < a.maxb ? trow[pidx] : -1;
                             if (id < 0 || id >= a.n_pages) {
@@ -409,130 +429,136 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                     }
                     return id;
                 };
+                // copies of this lane: page lane / NC, column lane % NC
+                const int off = (lane % C::NC) * (BK * 128) + (lane / C::NC) * (kPage * 128);
+                auto copy = [&](int i, int ids, const CUtensorMap *map, bool is_v) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (i % NB) * PG + (lane / C::NC) % PG);
+                    const int y = (id * a.hkv + w.seg_kvh) * kPage;
+                    const int key0 = (w.seg_blk + i) * BK;
+                    const int slot = seq % C::SLOTS;
+                    const uint32_t use = seq / C::SLOTS;
+                    if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], (use - 1) & 1))) {
+                        // (the ring cannot drain past a V block that was not handed on)
+                        flush();
+                        alive = alive &&
+                                __all_sync(0xffffffffu, mbar_wait(&empty[slot], (use - 1) & 1, a.status, a.wait_ns));
+                    }
+                    const bool clean = is_v && key0 + BK > w.seg_len - a.n_q;
+                    if (clean) flush();  // one at a time
+                    if (!alive) return;
+                    uint64_t *bar = clean ? tail : &full[slot];
+                    if (lane == 0) mbar_arrive_expect_tx(bar, C::SLOT);
+                    __syncwarp();
+                    if (lane < PG * C::NC) vtc::tma2d(skv + slot * C::SLOT + off, map, (lane % C::NC) * 64, y, bar);
+                    if (clean) {
+                        pend = {slot, key0, w.seg_len, seg};
+                        pending = true;
+                    }
+                    ++seq;
+                };
                 int cur = 0, nxt = load_ids(0);
-                for (int i = 0; i < w.sh.count && alive; ++i) {
+                for (int i = 0; i < w.seg_n && alive; ++i) {
                     if (i % NB == 0) {
                         cur = nxt;
                         nxt = load_ids(i + NB);
                     }
-                    // copies of this lane: page lane / NC, column lane % NC
-                    const int id = __shfl_sync(0xffffffffu, cur, (i % NB) * PG + (lane / C::NC) % PG);
-                    const int y = (id * a.hkv + w.seg_kvh) * kPage;
-                    const int off = (lane % C::NC) * (C::BK * 128) + (lane / C::NC) * (kPage * 128);
-                    const int key0 = (w.sh.first + i * w.sh.step) * C::BK;
-                    const bool in_tree = key0 + C::BK > w.seg_len - a.n_q;
-#pragma unroll
-                    for (int kv = 0; kv < 2; ++kv) {
-                        const int slot = seq % C::SLOTS;
-                        const uint32_t use = seq / C::SLOTS;
-                        if (use > 0 && !__all_sync(0xffffffffu, mbar_try_wait(&empty[slot], (use - 1) & 1))) {
-                            // (the ring cannot drain past a V block that was not handed on)
-                            flush();
-                            alive = alive && __all_sync(0xffffffffu, mbar_wait(&empty[slot], (use - 1) & 1, a.status,
-                                                                               a.wait_ns));
-                        }
-                        if (!alive) break;
-                        const bool clean = kv == 1 && in_tree;
-                        if (clean) flush();  // one at a time
-                        if (!alive) break;
-                        uint64_t *bar = clean ? tail : &full[slot];
-                        if (lane == 0) mbar_arrive_expect_tx(bar, C::SLOT);
-                        __syncwarp();
-                        if (lane < PG * C::NC)
-                            vtc::tma2d(skv + slot * C::SLOT + off, kv ? &a.vmap : &a.kmap, (lane % C::NC) * 64, y, bar);
-                        if (clean) {
-                            pend = {seq, key0, w.seg_len, seg};
-                            pending = true;
-                        }
-                        ++seq;
-                    }
+                    copy(i, cur, &a.kmap, false);
+                    if (alive) copy(i, cur, &a.vmap, true);
                 }
                 ++seg;
             }
             flush();
             // no copy may be under way when the CTA ends
-            for (uint32_t s = seq > C::SLOTS ? seq - C::SLOTS : 0; s < seq; ++s)
-                if ((int64_t)s != lost && !mbar_wait(&full[s % C::SLOTS], (s / C::SLOTS) & 1, a.status, a.wait_ns))
+            for (uint32_t q = seq > C::SLOTS ? seq - C::SLOTS : 0; q < seq; ++q)
+                if ((int)(q % C::SLOTS) != lost &&
+                    !mbar_wait(&full[q % C::SLOTS], (q / C::SLOTS) & 1, a.status, a.wait_ns))
                     break;
         }
-    } else if (warp == QT * 4 + 1) {
-        // ================= MMA issue (one thread) =================
-        if (lane == 0) {
-            uint32_t it = 0;
-            int seg = 0;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                alive = alive && mbar_wait(bar, parity, a.status, a.wait_ns);
-                vtc::tc_fence_after();
-                return alive;
-            };
-            auto k_seq = [](uint32_t n) { return 2 * n; };
-            auto issue_s = [&](uint32_t n, int t) {
-                const uint8_t *kt = skv + (k_seq(n) % C::SLOTS) * C::SLOT;
+    } else if (warp == C::SM_WARPS + 1) {
+        // ================= MMA issue (the warp in step, one elected thread) =================
+        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+        uint32_t seq = 0;            // copies taken from the ring
+        uint32_t done = 0, seg = 0;  // blocks and segments
+        // (a descriptor's address field counts 16 bytes: steps are added to it)
+        const uint64_t qd0 = vtc::sdesc(smem_u32(sq), 16, 1024);
+        const uint64_t kd0 = vtc::sdesc(smem_u32(skv), 16, 1024), vd0 = vtc::sdesc(smem_u32(skv), BK * 128, 1024);
+        auto issue_s = [&](int t, uint32_t slot) {
+            const uint64_t kd = kd0 + slot * (C::SLOT / 16), qd = qd0 + t * (C::QTILE / 16);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint64_t kd = vtc::sdesc(smem_u32(kt) + (ks >> 2) * (C::BK * 128) + (ks & 3) * 32, 16, 1024);
-                    if constexpr (C::QTM) {
-                        vtc::umma_ta(tmem + t * C::BK, tmem + C::Q_COL0 + ks * 8, kd, IQK, ks > 0);
-                    } else {
-                        const uint64_t qd = vtc::sdesc(
-                            smem_u32(sq + t * C::QTILE) + (ks >> 2) * (kTileRows * 128) + (ks & 3) * 32, 16, 1024);
-                        vtc::umma(tmem + t * C::BK, qd, kd, IQK, ks > 0);
-                    }
-                }
-                vtc::umma_commit(&s_ready[t]);
-            };
-            auto issue_pv = [&](uint32_t n, int t, bool add) {
-                const uint8_t *vt = skv + ((k_seq(n) + 1) % C::SLOTS) * C::SLOT;
-#pragma unroll
-                for (int kk = 0; kk < C::BK / 16; ++kk)
-                    vtc::umma_ta(tmem + C::O_COL0 + t * D, tmem + t * C::BK + kk * 8,
-                                 vtc::sdesc(smem_u32(vt) + kk * 16 * 128, C::BK * 128, 1024), IPV, add || kk > 0);
-            };
-            while (alive && w.next(a, glane)) {
-                const int n = w.sh.count;
-                if (!wait(&full[k_seq(it) % C::SLOTS], (k_seq(it) / C::SLOTS) & 1)) break;
-                for (int t = 0; t < nt && alive; ++t)
-                    if (wait(&q_ready[t], seg & 1)) issue_s(it, t);
-                if (!alive) break;
-                vtc::umma_commit(&empty[k_seq(it) % C::SLOTS]);
-                for (int j = 0; j < n && alive; ++j, ++it) {
-                    const uint32_t vs = k_seq(it) + 1, kn = k_seq(it + 1);
-                    const bool more = j + 1 < n;
-                    if (!wait(&full[vs % C::SLOTS], (vs / C::SLOTS) & 1)) break;
-                    for (int t = 0; t < nt && alive; ++t) {
-                        if (!wait(&p_ready[t], it & 1)) break;
-                        issue_pv(it, t, j > 0);
-                        if (more) {
-                            if (t == 0 && !wait(&full[kn % C::SLOTS], (kn / C::SLOTS) & 1)) break;
-                            issue_s(it + 1, t);
-                        } else {
-                            vtc::umma_commit(&o_done[t]);
-                        }
-                    }
-                    if (!alive) break;
-                    vtc::umma_commit(&empty[vs % C::SLOTS]);
-                    if (more) vtc::umma_commit(&empty[kn % C::SLOTS]);
-                }
-                ++seg;
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t ko = ((ks >> 2) * (BK * 128) + (ks & 3) * 32) / 16;
+                if constexpr (C::QTM)
+                    umma_ta(tmem + t * BK, tmem + C::Q_COL0 + ks * 8, kd + ko, IQK, ks > 0);
+                else
+                    umma(tmem + t * BK, qd + ((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) / 16, kd + ko, IQK, ks > 0);
             }
+            umma_commit(&s_ready[t]);
+        };
+        auto issue_pv = [&](int t, uint32_t slot, bool add) {
+            const uint64_t vd = vd0 + slot * (C::SLOT / 16);
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk)
+                umma_ta(tmem + C::O_COL0 + t * D, tmem + t * BK + kk * 8, vd + kk * 16 * 128 / 16, IPV, add || kk > 0);
+        };
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            alive = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_ns));
+            vtc::tc_fence_after();
+            return alive;
+        };
+        auto wait_copy = [&](uint32_t q) { return wait(&full[q % C::SLOTS], (q / C::SLOTS) & 1); };
+        while (alive && w.next(a)) {
+            const int n = w.seg_n;
+            if (!wait_copy(seq)) break;
+            for (int t = 0; t < nt && alive; ++t)
+                if (wait(&q_ready[t], seg & 1)) issue_s(t, seq % C::SLOTS);
+            if (!alive) break;
+            umma_commit(&empty[seq % C::SLOTS]);
+            ++seq;
+            for (int j = 0; j < n && alive; ++j) {
+                const bool more = j + 1 < n;
+                // both copies first: a wait or a commit between P V and S lets
+                // the tensor core run dry (64 keys, two tiles: 497 instead of
+                // 453 us at 131072 keys)
+                if (!wait_copy(seq) || (more && !wait_copy(seq + 1))) break;
+                for (int t = 0; t < nt; ++t) {
+                    if (!wait(&p_ready[t], done & 1)) break;
+                    issue_pv(t, seq % C::SLOTS, j > 0);
+                    if (more)
+                        issue_s(t, (seq + 1) % C::SLOTS);
+                    else
+                        umma_commit(&o_done[t]);
+                }
+                if (!alive) break;
+                ++done;
+                umma_commit(&empty[seq % C::SLOTS]);
+                ++seq;
+                if (more) {
+                    umma_commit(&empty[seq % C::SLOTS]);
+                    ++seq;
+                }
+            }
+            ++seg;
         }
+    } else if (QT == 2 && warp >= C::SM_WARPS) {
+        // (idle warps of that warpgroup)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     } else if ((warp >> 2) < nt) {
         // ================= softmax: one thread per row =================
+        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;  // row within the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lane_base + t * C::BK, t_o = tmem + lane_base + C::O_COL0 + t * D;
+        const uint32_t t_s = tmem + lane_base + t * BK, t_o = tmem + lane_base + C::O_COL0 + t * D;
         const int rg = (tile0 + t) * kTileRows + r;
         const bool rvalid = rg < a.n_q * a.grp;
         const int qi = rvalid ? rg / a.grp : 0, qn = rvalid ? rg % a.grp : 0;
-        uint32_t it = 0;
-        int seg = 0;
-        while (w.next(a, glane)) {
+        uint32_t it = 0, seg = 0;  // blocks and segments of this chain
+        for (; w.next(a); ++seg) {
             const int base = w.seg_len - a.n_q;
             const int64_t orow = ((int64_t)w.seg_b * a.n_q + qi) * a.hq + (int64_t)w.seg_kvh * a.grp + qn;
             unsigned long long mask = 0;
             if (alive) {
-                // this row of Q, to TMEM (as bf16 pairs) or to shared memory
+                // this row of Q, to TMEM as bf16 pairs or to shared memory
                 uint4 u[D / 8];
                 const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
 #pragma unroll
@@ -559,32 +585,36 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 vtc::tc_fence_before();
-                mbar_arrive(&q_ready[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_ready[t]);
             }
             float m_used = -INFINITY, l = 0.0f;
             // tcgen05.ld / st are warp-collective: every lane runs them together
-            for (int j = 0; j < w.sh.count && alive; ++j, ++it) {
+            for (int j = 0; j < w.seg_n && alive; ++j, ++it) {
                 alive = __all_sync(0xffffffffu, mbar_wait(&s_ready[t], it & 1, a.status, a.wait_ns));
                 if (!alive) break;
                 vtc::tc_fence_after();
-                float s[C::BK];
-                tmem_ld_block<C::BK>(t_s, s);
-                const int key0 = (w.sh.first + j * w.sh.step) * C::BK;
-                if (key0 + C::BK > base) {
+                float s[BK];
 #pragma unroll
-                    for (int h = 0; h < C::BK / 64; ++h) {
+                for (int h = 0; h < BK / 64; ++h)
+                    vtc::tmem_ld_row<64>(t_s + 64 * h, *reinterpret_cast<float(*)[64]>(&s[64 * h]));
+                const int key0 = (w.seg_blk + j) * BK;
+                if (key0 + BK > base) {
+#pragma unroll
+                    for (int h = 0; h < BK / 64; ++h) {
                         const unsigned long long seen = seen_bits(mask, key0 + 64 * h, base);
 #pragma unroll
                         for (int c = 0; c < 64; ++c)
                             if (!((seen >> c) & 1)) s[64 * h + c] = -INFINITY;
                     }
                 }
-                const float mb = vtc::max_tree<C::BK>(s) * a.scale_log2;
+                const float mb = max_of<BK>(s) * a.scale_log2;
                 // the reference maximum follows only rises of more than 2^8
                 // (rare after the first block): then O is rescaled
                 const bool grow = mb > m_used + 8.0f;
                 if (__any_sync(0xffffffffu, grow) && j > 0) {
                     const float f = grow ? (m_used == -INFINITY ? 0.0f : ex2(m_used - mb)) : 1.0f;
+#pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 16) {
                         float v[16];
                         vtc::tmem_ld16(t_o + c0, v);
@@ -598,22 +628,24 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 const float nms = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int h = 0; h < C::BK / 32; ++h) {
+                for (int h = 0; h < BK / 32; ++h) {
                     float pk[16];
 #pragma unroll
                     for (int c = 0; c < 16; ++c) {
-                        const float p0 = ex2(fmaf(s[h * 32 + 2 * c], a.scale_log2, nms));
-                        const float p1 = ex2(fmaf(s[h * 32 + 2 * c + 1], a.scale_log2, nms));
-                        ls[(2 * c) & 3] += p0;
-                        ls[(2 * c + 1) & 3] += p1;
+                        float p0, p1;
+                        fma2(p0, p1, s[h * 32 + 2 * c], s[h * 32 + 2 * c + 1], a.scale_log2, nms);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        add2(ls[(2 * c) & 2], ls[((2 * c) & 2) + 1], p0, p1);
                         pk[c] = __uint_as_float(pack_bf16(p0, p1));
                     }
                     vtc::tmem_st16_nowait(t_s + h * 16, pk);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
                 vtc::tc_fence_before();
-                mbar_arrive(&p_ready[t]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[t]);
+                l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
             }
             if (alive)
                 alive = __all_sync(0xffffffffu, mbar_wait(&o_done[t], seg & 1, a.status, a.wait_ns));
@@ -630,6 +662,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
             const bool zero = mask == 0 || (m_used == -INFINITY && l == 0.0f);
             const int64_t prow = ((int64_t)blockIdx.x * 2 + !w.at_start) * C::ROWS + t * kTileRows + r;
             const float f = 1.0f / l;
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 16) {
                 float v[16];
                 if (alive) {
@@ -642,10 +675,8 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 if (w.whole) {
                     store_out16<D>(a, orow, c0, v, f, zero);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        *reinterpret_cast<float4 *>(a.ws_o + prow * D + c0 + i) =
-                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    store_ws8(a.ws_o + prow * D + c0, v);
+                    store_ws8(a.ws_o + prow * D + c0 + 8, v + 8);
                 }
             }
             if (rvalid && !w.whole) {
@@ -653,7 +684,6 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
                 a.ws_ml[prow * 2 + 1] = zero ? 0.0f : l;
             }
             vtc::tc_fence_before();
-            ++seg;
         }
         pdl_trigger();
     }
@@ -666,22 +696,27 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem_raw) {
 
 // Join the partials of units that span several ranges, in range order, and
 // write zeros for requests that are refused.  One block per (unit, kJoinRows
-// rows), one warp per row in turn.
+// rows), a warp per row: the lanes read the partials' (m, l) side by side and
+// leave each partial's weight in shared memory, then run over the partial
+// outputs, eight loads in flight.
 constexpr int kJoinRows = 8;
+constexpr int kMaxPieces = 2 * kSMs;
 template <int D, int QT>
 __device__ __forceinline__ void tree_join_block(const Args &a) {
     using C = Cfg<D, QT>;
-    constexpr int E = D / 32;
-    __shared__ int64_t sums[4];
+    constexpr int BK = C::BK, E = D / 32, U = 8;
+    __shared__ int64_t sums[kJoinRows];
     __shared__ int64_t before_s;
+    __shared__ float weight[kJoinRows][kMaxPieces];
+    __shared__ int slot[kJoinRows][kMaxPieces];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int unit = blockIdx.x, b = unit / a.hkv, kvh = unit % a.hkv;
-    const int nblk = blocks_of<C::BK>(a, b);
+    const int nblk = blocks_of<BK>(a, b);
     if (nblk == 0 && tid == 0 && kvh == 0 && blockIdx.y == 0) report(a.status, VC_ERR_BAD_INDEX);
-    const Sums sm = sum_blocks<C::BK>(a, sums, tid, 128);
+    const Sums sm = sum_blocks<BK>(a, sums, tid, kJoinRows * 32);
     if (b >= sm.b0 && b < sm.b1) {
         int64_t p = sm.before;
-        for (int i = sm.b0; i < b; ++i) p += blocks_of<C::BK>(a, i);
+        for (int i = sm.b0; i < b; ++i) p += blocks_of<BK>(a, i);
         before_s = p;
     }
     __syncthreads();
@@ -693,45 +728,66 @@ __device__ __forceinline__ void tree_join_block(const Args &a) {
         g1 = (int)((u1 * a.groups - 1) / total);
         if (g0 == g1) return;  // finished there
     }
-    for (int k = warp; k < kJoinRows; k += 4) {
-        const int rg = blockIdx.y * kJoinRows + k;
-        if (rg >= a.n_q * a.grp) return;
-        const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
-        const int tile = rg / kTileRows;
-        // the CTAs of a group that hold this tile
-        const bool pair = QT == 2 && a.lanes == 3 && tile < 2;
-        const int lane0 = QT == 1 || pair ? 0 : a.lanes == 3 ? 2 : tile / 2;
-        const int trow = (QT == 1 ? 0 : a.lanes == 3 && tile == 2 ? 0 : (tile & 1)) * kTileRows + rg % kTileRows;
-        float M = -INFINITY, L = 0.0f, acc[E];
+    const int rr = blockIdx.y * kJoinRows + warp, rg = a.tile0 * kTileRows + rr;
+    if (rg >= min(a.n_q * a.grp, a.tiles * kTileRows)) return;
+    const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
+    // where a group's partials of this row are
+    const int cta = rr / C::ROWS, trow = rr % C::ROWS, n = g1 - g0 + 1;
+    float M = -INFINITY;
+    for (int p = lane; p < n; p += 32) {
+        const int g = g0 + p;
+        const int64_t s0 = range_start(total, g, a.groups), s1 = range_start(total, g + 1, a.groups);
+        const bool any = s0 < s1;
+        const int pr = any ? ((g * a.lanes + cta) * 2 + (u0 > s0)) * C::ROWS + trow : -1;
+        slot[warp][p] = pr;
+        weight[warp][p] = any ? a.ws_ml[(int64_t)pr * 2] : -INFINITY;
+        M = fmaxf(M, weight[warp][p]);
+    }
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.0f, acc[E];
 #pragma unroll
-        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-        for (int g = g0; g <= g1; ++g) {
-            const int64_t s0 = range_start(total, g, a.groups), s1 = range_start(total, g + 1, a.groups);
-            const int64_t lo = max(u0, s0), hi = min(u1, s1);
-            for (int ln = 0; ln < (pair ? 2 : 1); ++ln) {
-                if (share_of(a.lanes, lane0 + ln, unit, (int)(lo - u0), (int)(hi - lo), false).count == 0) continue;
-                const int64_t prow =
-                    (((int64_t)g * a.lanes + lane0 + ln) * 2 + (lo != s0)) * C::ROWS + trow;
-                const float m = a.ws_ml[prow * 2], l = a.ws_ml[prow * 2 + 1];
-                const float mn = fmaxf(M, m);
-                if (mn == -INFINITY) continue;
-                const float fo = ex2(M - mn), fn = ex2(m - mn);
-                M = mn;
-                L = L * fo + l * fn;
-                const float *o = a.ws_o + prow * D + lane * E;
+    for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+    if (M != -INFINITY) {
+        for (int p = lane; p < n; p += 32) {
+            const float w = weight[warp][p] == -INFINITY ? 0.0f : ex2(weight[warp][p] - M);
+            weight[warp][p] = w;
+            if (slot[warp][p] >= 0 && w != 0.0f) L += w * a.ws_ml[(int64_t)slot[warp][p] * 2 + 1];
+        }
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        __syncwarp();
+        for (int p0 = 0; p0 < n; p0 += U) {
+            float o[U][E];
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = acc[i] * fo + o[i] * fn;
+            for (int k = 0; k < U; ++k) {
+                // (a partial without weight holds nothing to read)
+                const bool in = p0 + k < n && weight[warp][p0 + k] != 0.0f;
+                const float *src = a.ws_o + (in ? (int64_t)slot[warp][p0 + k] : 0) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 q = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    o[k][0] = q.x; o[k][1] = q.y; o[k][2] = q.z; o[k][3] = q.w;
+                } else {
+                    const float2 q = in ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
+                    o[k][0] = q.x; o[k][1] = q.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                const float w = p0 + k < n ? weight[warp][p0 + k] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(w, o[k][i], acc[i]);
             }
         }
-        const float f = M == -INFINITY ? 0.0f : 1.0f / L;
+    }
+    const float f = M == -INFINITY ? 0.0f : 1.0f / L;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float y = M == -INFINITY ? 0.0f : acc[i] * f;
-            if (a.out_bf16)
-                ((uint16_t *)a.out)[orow * D + lane * E + i] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
-            else
-                ((float *)a.out)[orow * D + lane * E + i] = y;
-        }
+    for (int i = 0; i < E; ++i) acc[i] *= f;
+    if (a.out_bf16) {
+        uint32_t *dst = reinterpret_cast<uint32_t *>((uint16_t *)a.out + orow * D + lane * E);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) dst[i] = pack_bf16(acc[2 * i], acc[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) ((float *)a.out)[orow * D + lane * E + i] = acc[i];
     }
 }
 

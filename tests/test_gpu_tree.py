@@ -94,7 +94,7 @@ def test_tree_attention(hq, hkv, d, n_q, pre, dtype):
         check_attn(out, hf, qn, masks[b], scale, b)
 
 
-@pytest.mark.parametrize("n_q,hq,hkv", [(25, 8, 2), (64, 8, 1)])
+@pytest.mark.parametrize("n_q,hq,hkv", [(25, 8, 2), (40, 8, 1), (64, 8, 1), (60, 10, 2)])
 def test_long_ragged_batch(n_q, hq, hkv):
     """Contexts of many splits beside short ones; every row checked."""
     rng = np.random.default_rng([n_q, hq])
