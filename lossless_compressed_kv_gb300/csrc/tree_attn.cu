@@ -18,9 +18,10 @@ __global__ void __launch_bounds__(tree::Cfg<D, QT>::THREADS, tree::Cfg<D, QT>::M
 }
 
 template <int D, int QT>
-__global__ void __launch_bounds__(tree::kJoinRows * 32) tree_join_kernel(const __grid_constant__ tree::Args a) {
+__global__ void __launch_bounds__(tree::kJoinWarps * 32)
+    tree_join_kernel(const __grid_constant__ tree::Args a, int warps_per_row) {
     pdl_begin();
-    tree::tree_join_block<D, QT>(a);
+    tree::tree_join_block<D, QT>(a, warps_per_row);
 }
 
 // How a launch is laid out over the GPU; a call takes one, or two for three
@@ -62,8 +63,10 @@ cudaError_t launch(const tree::Args &a, cudaStream_t st) {
     e = launch_pdl(tree_kernel<D, QT>, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
     if (e != cudaSuccess) return e;
     const int rows = min(a.n_q * a.grp, a.tiles * tree::kTileRows) - a.tile0 * tree::kTileRows;
-    const dim3 grid(a.batch * a.hkv, ceil_div(rows, tree::kJoinRows));
-    e = launch_pdl(tree_join_kernel<D, QT>, grid, tree::kJoinRows * 32, 0, st, a);
+    // ranges that a unit spans, were the lengths alike: a warp reads eight at once
+    const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
+    const dim3 grid(a.batch * a.hkv, ceil_div(rows, tree::kJoinWarps / W));
+    e = launch_pdl(tree_join_kernel<D, QT>, grid, tree::kJoinWarps * 32, 0, st, a, W);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

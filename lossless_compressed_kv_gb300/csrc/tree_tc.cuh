@@ -87,7 +87,7 @@ struct Cfg {
     static constexpr int OFF_BAR = OFF_KV + SLOTS * SLOT;
     static constexpr int NBAR = 4 * QT + 2 * SLOTS + 1;  // q, s, p, o per tile; full, empty; tail
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-    static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 64 * 4;
+    static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 16;
     static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "shared memory of the CTAs an SM holds");
     // TMEM columns: S (then P) and O of each tile, Q (bf16 pairs)
     static constexpr int O_COL0 = QT * BK;
@@ -112,59 +112,77 @@ __device__ inline int blocks_of(const Args &a, int b) {
     return len >= a.n_q && len <= a.max_len ? ceil_div(len, BK) : 0;
 }
 
-// Sums over the batch in one go: the blocks of all requests and those of the
-// requests before b_until; a thread takes a run of `per` requests, and `mine`
-// / `before` are its run's blocks and those before its run.
-struct Sums {
-    int64_t total, before, mine;
-    int b0, b1;
+// How the blocks of all units, laid end to end, are dealt out: T = q G + r,
+// the first r groups take q + 1 blocks and the others q.  (T is below 2^31:
+// K and V of 2^31 blocks would fill 70 TB.)
+struct Deal {
+    int q, r;
+    __device__ Deal(int total, int groups) : q(total / groups), r(total % groups) {}
+    __device__ int start(int g) const { return g * q + min(g, r); }
+    __device__ int group_of(int block) const {
+        const int split = r * (q + 1);
+        return block < split ? block / (q + 1) : r + (block - split) / q;
+    }
 };
+
+// Blocks (of one kv head) of all requests and of those before request
+// `until`: every warp adds them up for itself, a lane per request.
 template <int BK>
-__device__ inline Sums sum_blocks(const Args &a, int64_t *sh, int tid, int nthreads) {
-    Sums s;
-    const int per = ceil_div(a.batch, nthreads), lane = tid & 31, warp = tid >> 5;
-    s.b0 = min(a.batch, tid * per);
-    s.b1 = min(a.batch, s.b0 + per);
-    s.mine = 0;
-    for (int b = s.b0; b < s.b1; ++b) s.mine += blocks_of<BK>(a, b);
-    int64_t inc = s.mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+__device__ inline void sum_blocks(const Args &a, int until, int lane, int &total, int &before) {
+    total = before = 0;
+    for (int b = lane; b < a.batch; b += 32) {
+        const int n = blocks_of<BK>(a, b);
+        total += n;
+        before += b < until ? n : 0;
     }
-    if (lane == 31) sh[warp] = inc;
-    __syncthreads();
-    s.before = inc - s.mine;
-    s.total = 0;
-    for (int w = 0; w < nthreads / 32; ++w) {
-        if (w < warp) s.before += sh[w];
-        s.total += sh[w];
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    return s;
 }
 
-// The range of group g among G: blocks [g T / G, (g + 1) T / G) of T.
-__host__ __device__ inline int64_t range_start(int64_t total, int g, int groups) { return total * g / groups; }
+// The request that holds block f of the blocks laid end to end, and the block's
+// place among that request's (all kv heads); by a warp.
+template <int BK>
+__device__ inline void find_block(const Args &a, int f, int lane, int &b, int &rest) {
+    int before = 0;
+    for (int b0 = 0;; b0 += 32) {
+        const int n = b0 + lane < a.batch ? blocks_of<BK>(a, b0 + lane) * a.hkv : 0;
+        int upto = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, f < before + upto);
+        if (here) {
+            const int first = __ffs(here) - 1;
+            b = b0 + first;
+            rest = f - before - __shfl_sync(0xffffffffu, upto - n, first);
+            return;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+}
 
 // A group's walk through its range.
 template <int BK>
 struct Walk {
     int b, kvh, blk, nblk, len;
-    int64_t left;
+    int left;
     bool first;
     // the current segment
     int seg_b, seg_kvh, seg_len, seg_blk, seg_n;
     bool whole, at_start;
 
-    __device__ void begin(const Args &a, int b_, int kvh_, int blk_, int64_t left_) {
+    __device__ void begin(const Args &a, int b_, int rest, int left_) {
         b = b_;
-        kvh = kvh_;
-        blk = blk_;
         left = left_;
         first = true;
         if (left > 0) {
             nblk = blocks_of<BK>(a, b);
             len = a.lens[b];
+            kvh = rest / nblk;
+            blk = rest % nblk;
         }
     }
     // The next segment.
@@ -179,7 +197,7 @@ struct Walk {
                 len = a.lens[b];
             }
         }
-        seg_n = (int)min((int64_t)(nblk - blk), left);
+        seg_n = min(nblk - blk, left);
         whole = seg_n == nblk;
         at_start = first;
         seg_b = b;
@@ -306,10 +324,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + QT, *o_done = p_ready + QT;
     uint64_t *full = o_done + QT, *empty = full + C::SLOTS, *tail = empty + C::SLOTS;
     unsigned long long *bad = reinterpret_cast<unsigned long long *>(smem + C::OFF_MISC);  // [kBadRing]
-    int32_t *misc = reinterpret_cast<int32_t *>(bad + kBadRing);  // 64 words
-    uint32_t *tslot = reinterpret_cast<uint32_t *>(misc);
-    int *where = misc + 2;                                        // first request, kv head, block
-    int64_t *sums = reinterpret_cast<int64_t *>(misc + 8);        // one per warp
+    uint32_t *tslot = reinterpret_cast<uint32_t *>(bad + kBadRing);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp_id = blockIdx.x / a.lanes, glane = blockIdx.x % a.lanes;
@@ -338,25 +353,17 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     vtc::tc_fence_before();
-    const Sums sm = sum_blocks<BK>(a, sums, tid, C::THREADS);  // (holds a __syncthreads)
-    const int64_t total = sm.total * a.hkv;
-    const int64_t f0 = range_start(total, grp_id, a.groups), f1 = range_start(total, grp_id + 1, a.groups);
-    if (f0 < f1 && f0 >= sm.before * a.hkv && f0 < (sm.before + sm.mine) * a.hkv) {
-        int64_t rem = f0 - sm.before * a.hkv;
-        int b = sm.b0, n = blocks_of<BK>(a, b);
-        while (rem >= (int64_t)n * a.hkv) {
-            rem -= (int64_t)n * a.hkv;
-            n = blocks_of<BK>(a, ++b);
-        }
-        where[0] = b;
-        where[1] = (int)(rem / n);
-        where[2] = (int)(rem % n);
-    }
+    // this group's range, by every warp for itself
+    int total, before, b0 = 0, rest = 0;
+    sum_blocks<BK>(a, 0, lane, total, before);
+    const Deal deal(total * a.hkv, a.groups);
+    const int f0 = deal.start(grp_id), mine = deal.start(grp_id + 1) - f0;
+    if (mine > 0) find_block<BK>(a, f0, lane, b0, rest);
+    Walk<BK> w;
+    w.begin(a, b0, rest, mine);
     __syncthreads();
     vtc::tc_fence_after();
     const uint32_t tmem = *tslot;
-    Walk<BK> w;
-    w.begin(a, f0 < f1 ? where[0] : 0, f0 < f1 ? where[1] : 0, f0 < f1 ? where[2] : 0, f1 - f0);
 
     constexpr uint32_t IQK = vtc::idesc_bf16(128, BK, false);
     constexpr uint32_t IPV = vtc::idesc_bf16(128, D, true);
@@ -694,93 +701,100 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS));
 }
 
-// Join the partials of units that span several ranges, in range order, and
-// write zeros for requests that are refused.  One block per (unit, kJoinRows
-// rows), a warp per row: the lanes read the partials' (m, l) side by side and
-// leave each partial's weight in shared memory, then run over the partial
-// outputs, eight loads in flight.
-constexpr int kJoinRows = 8;
-constexpr int kMaxPieces = 2 * kSMs;
+// Join the partials of units that span several ranges, and write zeros for
+// requests that are refused.  One block per (unit, kJoinWarps / W rows): W warps
+// share a row and take every W-th range each (a running maximum and sum, eight
+// partials read at once), in an order that the lengths alone fix.
+constexpr int kJoinWarps = 8;
 template <int D, int QT>
-__device__ __forceinline__ void tree_join_block(const Args &a) {
+__device__ __forceinline__ void tree_join_block(const Args &a, int W) {
     using C = Cfg<D, QT>;
     constexpr int BK = C::BK, E = D / 32, U = 8;
-    __shared__ int64_t sums[kJoinRows];
-    __shared__ int64_t before_s;
-    __shared__ float weight[kJoinRows][kMaxPieces];
-    __shared__ int slot[kJoinRows][kMaxPieces];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float part[kJoinWarps][E + 2][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int unit = blockIdx.x, b = unit / a.hkv, kvh = unit % a.hkv;
     const int nblk = blocks_of<BK>(a, b);
-    if (nblk == 0 && tid == 0 && kvh == 0 && blockIdx.y == 0) report(a.status, VC_ERR_BAD_INDEX);
-    const Sums sm = sum_blocks<BK>(a, sums, tid, kJoinRows * 32);
-    if (b >= sm.b0 && b < sm.b1) {
-        int64_t p = sm.before;
-        for (int i = sm.b0; i < b; ++i) p += blocks_of<BK>(a, i);
-        before_s = p;
-    }
-    __syncthreads();
-    const int64_t total = sm.total * a.hkv, u0 = before_s * a.hkv + (int64_t)kvh * nblk, u1 = u0 + nblk;
+    if (nblk == 0 && threadIdx.x == 0 && kvh == 0 && blockIdx.y == 0) report(a.status, VC_ERR_BAD_INDEX);
+    int total, before;
+    sum_blocks<BK>(a, b, lane, total, before);
+    const Deal deal(total * a.hkv, a.groups);
+    const int u0 = before * a.hkv + kvh * nblk;
     // groups whose ranges hold the unit's first and last block
-    int g0 = 0, g1 = -1;
-    if (nblk > 0) {
-        g0 = (int)(((u0 + 1) * a.groups - 1) / total);
-        g1 = (int)((u1 * a.groups - 1) / total);
-        if (g0 == g1) return;  // finished there
-    }
-    const int rr = blockIdx.y * kJoinRows + warp, rg = a.tile0 * kTileRows + rr;
-    if (rg >= min(a.n_q * a.grp, a.tiles * kTileRows)) return;
-    const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
-    // where a group's partials of this row are
-    const int cta = rr / C::ROWS, trow = rr % C::ROWS, n = g1 - g0 + 1;
-    float M = -INFINITY;
-    for (int p = lane; p < n; p += 32) {
-        const int g = g0 + p;
-        const int64_t s0 = range_start(total, g, a.groups), s1 = range_start(total, g + 1, a.groups);
-        const bool any = s0 < s1;
-        const int pr = any ? ((g * a.lanes + cta) * 2 + (u0 > s0)) * C::ROWS + trow : -1;
-        slot[warp][p] = pr;
-        weight[warp][p] = any ? a.ws_ml[(int64_t)pr * 2] : -INFINITY;
-        M = fmaxf(M, weight[warp][p]);
-    }
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.0f, acc[E];
+    const int g0 = nblk > 0 ? deal.group_of(u0) : 0, g1 = nblk > 0 ? deal.group_of(u0 + nblk - 1) : -1;
+    if (nblk > 0 && g0 == g1) return;  // finished there
+    const int rr = blockIdx.y * (kJoinWarps / W) + warp / W, rg = a.tile0 * kTileRows + rr;
+    const bool row_ok = rg < min(a.n_q * a.grp, a.tiles * kTileRows);
+    const int cta = rr / C::ROWS, trow = rr % C::ROWS;
+    float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-    if (M != -INFINITY) {
-        for (int p = lane; p < n; p += 32) {
-            const float w = weight[warp][p] == -INFINITY ? 0.0f : ex2(weight[warp][p] - M);
-            weight[warp][p] = w;
-            if (slot[warp][p] >= 0 && w != 0.0f) L += w * a.ws_ml[(int64_t)slot[warp][p] * 2 + 1];
-        }
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        __syncwarp();
-        for (int p0 = 0; p0 < n; p0 += U) {
-            float o[U][E];
+    if (row_ok) {
+        for (int gb = g0 + warp % W; gb <= g1; gb += U * W) {
+            float m[U], l[U], o[U][E];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                // (a partial without weight holds nothing to read)
-                const bool in = p0 + k < n && weight[warp][p0 + k] != 0.0f;
-                const float *src = a.ws_o + (in ? (int64_t)slot[warp][p0 + k] : 0) * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 q = in ? *reinterpret_cast<const float4 *>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    o[k][0] = q.x; o[k][1] = q.y; o[k][2] = q.z; o[k][3] = q.w;
-                } else {
-                    const float2 q = in ? *reinterpret_cast<const float2 *>(src) : make_float2(0.f, 0.f);
-                    o[k][0] = q.x; o[k][1] = q.y;
+                const int g = gb + k * W;
+                m[k] = -INFINITY;
+                l[k] = 0.0f;
+#pragma unroll
+                for (int i = 0; i < E; ++i) o[k][i] = 0.0f;
+                if (g <= g1) {
+                    // (ranges between the first and the last are never empty)
+                    const int64_t pr = ((int64_t)(g * a.lanes + cta) * 2 + (u0 > deal.start(g))) * C::ROWS + trow;
+                    const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + pr * 2);
+                    m[k] = ml.x;
+                    l[k] = ml.y;
+                    const float *src = a.ws_o + pr * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 q = *reinterpret_cast<const float4 *>(src);
+                        o[k][0] = q.x; o[k][1] = q.y; o[k][2] = q.z; o[k][3] = q.w;
+                    } else {
+                        const float2 q = *reinterpret_cast<const float2 *>(src);
+                        o[k][0] = q.x; o[k][1] = q.y;
+                    }
                 }
             }
+            float mx = M;
+#pragma unroll
+            for (int k = 0; k < U; ++k) mx = fmaxf(mx, m[k]);
+            if (mx == -INFINITY) continue;
+            const float f = ex2(M - mx);
+            M = mx;
+            L *= f;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] *= f;
 #pragma unroll
             for (int k = 0; k < U; ++k) {
-                const float w = p0 + k < n ? weight[warp][p0 + k] : 0.0f;
+                if (m[k] == -INFINITY) continue;  // (such a partial's sums are not to be used)
+                const float wk = ex2(m[k] - mx);
+                L = fmaf(wk, l[k], L);
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(w, o[k][i], acc[i]);
+                for (int i = 0; i < E; ++i) acc[i] = fmaf(wk, o[k][i], acc[i]);
             }
         }
     }
+    if (W > 1) {
+        part[warp][0][lane] = M;
+        part[warp][1][lane] = L;
+#pragma unroll
+        for (int i = 0; i < E; ++i) part[warp][2 + i][lane] = acc[i];
+        __syncthreads();
+        if (warp % W) return;
+        for (int k = 1; k < W; ++k) {
+            const float m = part[warp + k][0][lane], mx = fmaxf(M, m);
+            if (m == -INFINITY) continue;
+            const float f = ex2(M - mx), wk = ex2(m - mx);
+            M = mx;
+            L = L * f + part[warp + k][1][lane] * wk;
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + part[warp + k][2 + i][lane] * wk;
+        }
+    }
+    if (!row_ok) return;
+    const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
     const float f = M == -INFINITY ? 0.0f : 1.0f / L;
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] *= f;
+    for (int i = 0; i < E; ++i) acc[i] = M == -INFINITY ? 0.0f : acc[i] * f;
     if (a.out_bf16) {
         uint32_t *dst = reinterpret_cast<uint32_t *>((uint16_t *)a.out + orow * D + lane * E);
 #pragma unroll
