@@ -463,31 +463,50 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 
-def _need(name: str, t, dtype, shape):
-    """A contiguous tensor of this type and shape on the current device."""
+# These wrappers run once per layer and step: pointers go to ctypes as plain
+# integers, the current device and stream are read once a call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
+def _need(name: str, t, dtype, shape, dev: int):
+    """The address of a contiguous tensor of this type and shape on device dev."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
-    _here(name, t)
+    return _here(name, t, dev)
 
 
-def _here(name: str, t):
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _here(name: str, t, dev: int):
+    if not t.is_cuda or t.get_device() != dev:
         raise ValueError("%s must be on the current CUDA device" % name)
+    return t.data_ptr()
 
 
-def _status(status):
-    if status is not None:
-        _need("status", status, _I32, (1,))
-    return _ptr(status)
+def _status(status, dev: int):
+    return None if status is None else _need("status", status, _I32, (1,), dev)
 
 
-def _cache(full: PagedKV):
-    """The struct of a cache whose four tensors are on the current device."""
-    for name in ("k_pages", "v_pages", "block_table", "seq_lens"):
-        _here(name, getattr(full, name))
-    if full.seq_lens.shape != full.block_table.shape[:1] or full.v_pages.shape[0] != full.k_pages.shape[0]:
-        raise ValueError("block_table, seq_lens and the page pools disagree in size")
-    return full.struct()
+def _on(stream, dev: int):
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("stream must be one of the current CUDA device")
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _cache(kv: PagedKV, dev: int) -> PagedKVStruct:
+    """The struct of a cache whose four tensors are contiguous on device dev."""
+    k, v, table, lens = kv.k_pages, kv.v_pages, kv.block_table, kv.seq_lens
+    b, w = table.shape
+    n = k.shape[0]
+    if v.shape[0] != n or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError("the page pools must be contiguous and of one size")
+    return PagedKVStruct(_here("k_pages", k, dev), _here("v_pages", v, dev), n,
+                         _need("block_table", table, _I32, (b, w), dev), _need("seq_lens", lens, _I32, (b,), dev), b, w,
+                         KVFormat(kv.num_kv_heads, kv.head_dim, kv.bits))
 
 
 @dataclass(frozen=True)
@@ -517,31 +536,27 @@ def rotary_kv_write(qkv, row_req, row_pos, num_q_heads: int, rotary: Rotary, q_o
     qkv: fp32 or bf16 [m][(Hq + 2 Hkv) D], rows may be strided."""
     m, width = qkv.shape
     hkv, d = full.num_kv_heads, full.head_dim
-    dt = _DTYPES.get(qkv.dtype, -1)
     if width != (num_q_heads + 2 * hkv) * d or (width > 1 and qkv.stride(1) != 1):
         raise ValueError("qkv must be [m][(Hq + 2 Hkv) head_dim] with contiguous rows")
-    _here("qkv", qkv)
-    _need("row_req", row_req, _I32, (m,))
-    _need("row_pos", row_pos, _I32, (m,))
-    if row_slot is not None:
-        _need("row_slot", row_slot, _I32, (m,))
-    _need("q_out", q_out, _BF16, (m, num_q_heads, d))
-    fs, rs = _cache(full), rotary.struct()
-    _check(_lib.vc_rotary_kv_write(_ptr(qkv), dt, qkv.stride(0) if m > 1 else width, m, _ptr(row_req), _ptr(row_pos),
-                                   _ptr(row_slot), int(num_q_heads), C.byref(rs), _ptr(q_out), C.byref(fs),
-                                   _status(status), _stream(stream)), "vc_rotary_kv_write")
+    dev, rows = _device(), (m,)
+    fs, rs = _cache(full, dev), rotary.struct()
+    _check(_lib.vc_rotary_kv_write(
+        _here("qkv", qkv, dev), _DTYPES.get(qkv.dtype, -1), qkv.stride(0) if m > 1 else width, m,
+        _need("row_req", row_req, _I32, rows, dev), _need("row_pos", row_pos, _I32, rows, dev),
+        None if row_slot is None else _need("row_slot", row_slot, _I32, rows, dev), num_q_heads, C.byref(rs),
+        _need("q_out", q_out, _BF16, (m, num_q_heads, d), dev), C.byref(fs), _status(status, dev), _on(stream, dev)),
+        "vc_rotary_kv_write")
 
 
 def tree_plan(parent, seq_lens, mask, position, status=None, stream=None):
     """vc_tree_plan: parent int32 [B][n_q] -> mask int64 [B][n_q] (the node
     and its ancestors, one bit each) and position int32 [B][n_q]."""
-    b, n_q = parent.shape
-    _need("parent", parent, _I32, (b, n_q))
-    _need("seq_lens", seq_lens, _I32, (b,))
-    _need("mask", mask, _I64, (b, n_q))
-    _need("position", position, _I32, (b, n_q))
-    _check(_lib.vc_tree_plan(_ptr(parent), b, n_q, _ptr(seq_lens), _ptr(mask), _ptr(position), _status(status),
-                             _stream(stream)), "vc_tree_plan")
+    dev, shape = _device(), parent.shape
+    b, n_q = shape
+    _check(_lib.vc_tree_plan(
+        _need("parent", parent, _I32, shape, dev), b, n_q, _need("seq_lens", seq_lens, _I32, (b,), dev),
+        _need("mask", mask, _I64, shape, dev), _need("position", position, _I32, shape, dev), _status(status, dev),
+        _on(stream, dev)), "vc_tree_plan")
 
 
 def tree_workspace_bytes(full: PagedKV, n_q: int, num_q_heads: int, max_seq_len: int) -> int:
@@ -553,29 +568,26 @@ def tree_attn(q, full: PagedKV, mask, softmax_scale: float, out, max_seq_len: in
               stream=None):
     """vc_tree_attn: q bf16 [B][n_q][Hq][D] over KV_full, the last n_q entries
     of which are a tree; out fp32 or bf16 of the same shape."""
-    b, n_q, hq, d = q.shape
+    shape = q.shape
+    b, n_q, hq, d = shape
     if b != full.batch or d != full.head_dim:
         raise ValueError("q must be [batch][n_q][num_q_heads][head_dim] of the cache")
-    _need("q", q, _BF16, q.shape)
-    _need("mask", mask, _I64, (b, n_q))
-    _need("out", out, out.dtype, q.shape)
-    _here("workspace", workspace)
-    fs = _cache(full)
-    _check(_lib.vc_tree_attn(_ptr(q), n_q, hq, C.byref(fs), _ptr(mask), float(softmax_scale), _ptr(out),
-                             _DTYPES.get(out.dtype, -1), int(max_seq_len), _ptr(workspace),
-                             workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
-           "vc_tree_attn")
+    dev = _device()
+    fs = _cache(full, dev)
+    _check(_lib.vc_tree_attn(
+        _need("q", q, _BF16, shape, dev), n_q, hq, C.byref(fs), _need("mask", mask, _I64, (b, n_q), dev), softmax_scale,
+        _need("out", out, out.dtype, shape, dev), _DTYPES.get(out.dtype, -1), max_seq_len,
+        _here("workspace", workspace, dev), workspace.nbytes, _status(status, dev), _on(stream, dev)), "vc_tree_attn")
 
 
 def tree_accept(parent, tokens, verified, accept_len, path, emitted, stream=None):
     """vc_tree_accept: the greedy walk; all int32 [B][n_q], accept_len [B]."""
-    b, n_q = parent.shape
-    for name, t in (("parent", parent), ("tokens", tokens), ("verified", verified), ("path", path),
-                    ("emitted", emitted)):
-        _need(name, t, _I32, (b, n_q))
-    _need("accept_len", accept_len, _I32, (b,))
-    _check(_lib.vc_tree_accept(_ptr(parent), _ptr(tokens), _ptr(verified), b, n_q, _ptr(accept_len), _ptr(path),
-                               _ptr(emitted), _stream(stream)), "vc_tree_accept")
+    dev, shape = _device(), parent.shape
+    b, n_q = shape
+    p = [_need(name, t, _I32, shape, dev) for name, t in (("parent", parent), ("tokens", tokens), ("verified", verified),
+                                                          ("path", path), ("emitted", emitted))]
+    _check(_lib.vc_tree_accept(p[0], p[1], p[2], b, n_q, _need("accept_len", accept_len, _I32, (b,), dev), p[3], p[4],
+                               _on(stream, dev)), "vc_tree_accept")
 
 
 class KVLayers:
@@ -584,7 +596,8 @@ class KVLayers:
 
     def __init__(self, caches):
         self.caches = list(caches)
-        self.structs = (PagedKVStruct * len(self.caches))(*[_cache(c) for c in self.caches])
+        self.device = _device()
+        self.structs = (PagedKVStruct * len(self.caches))(*[_cache(c, self.device) for c in self.caches])
 
     def __len__(self):
         return len(self.caches)
@@ -593,13 +606,13 @@ class KVLayers:
 def tree_commit(layers: KVLayers, accept_len, path, status=None, stream=None):
     """vc_tree_commit: move the accepted path's K / V to where a chain would
     have put them, in every layer."""
-    b, n_q = path.shape
-    if len(layers) and layers.caches[0].batch != b:
-        raise ValueError("path must be [batch][n_q] of the caches")
-    _need("accept_len", accept_len, _I32, (b,))
-    _need("path", path, _I32, (b, n_q))
-    _check(_lib.vc_tree_commit(layers.structs, len(layers), n_q, _ptr(accept_len), _ptr(path), _status(status),
-                               _stream(stream)), "vc_tree_commit")
+    dev, shape = _device(), path.shape
+    b, n_q = shape
+    if len(layers) and (layers.caches[0].batch != b or layers.device != dev):
+        raise ValueError("path must be [batch][n_q] of the caches, which must be on the current CUDA device")
+    _check(_lib.vc_tree_commit(
+        layers.structs, len(layers), n_q, _need("accept_len", accept_len, _I32, (b,), dev),
+        _need("path", path, _I32, shape, dev), _status(status, dev), _on(stream, dev)), "vc_tree_commit")
 
 
 def token_logprobs_workspace_bytes(rows: int, vocab: int, top_k: int) -> int:
@@ -615,23 +628,19 @@ def token_logprobs(logits, ids, logprobs, workspace, temperature: float = 1.0, e
     rows, vocab = logits.shape
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("the rows of logits must be contiguous")
-    _here("logits", logits)
-    n_ids = ids.shape[1]
-    _need("ids", ids, _I32, (rows, n_ids))
-    _need("logprobs", logprobs, _F32, (rows, n_ids))
-    if entropy is not None:
-        _need("entropy", entropy, _F32, (rows,))
-    k = 0
+    dev = _device()
+    n_ids, k, ti, tl = ids.shape[1], 0, None, None
     if top_ids is not None:
         k = top_ids.shape[1]
-        _need("top_ids", top_ids, _I32, (rows, k))
-        _need("top_logprobs", top_logprobs, _F32, (rows, k))
-    _here("workspace", workspace)
-    _check(_lib.vc_token_logprobs(_ptr(logits), _DTYPES.get(logits.dtype, -1), rows, vocab,
-                                  logits.stride(0) if rows > 1 else vocab, _ptr(ids), n_ids, float(temperature), k,
-                                  _ptr(logprobs), _ptr(entropy), _ptr(top_ids), _ptr(top_logprobs), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _status(status), _stream(stream)),
-           "vc_token_logprobs")
+        ti = _need("top_ids", top_ids, _I32, (rows, k), dev)
+        tl = _need("top_logprobs", top_logprobs, _F32, (rows, k), dev)
+    _check(_lib.vc_token_logprobs(
+        _here("logits", logits, dev), _DTYPES.get(logits.dtype, -1), rows, vocab, logits.stride(0) if rows > 1 else vocab,
+        _need("ids", ids, _I32, (rows, n_ids), dev), n_ids, temperature, k,
+        _need("logprobs", logprobs, _F32, (rows, n_ids), dev),
+        None if entropy is None else _need("entropy", entropy, _F32, (rows,), dev), ti, tl,
+        _here("workspace", workspace, dev), workspace.nbytes, _status(status, dev), _on(stream, dev)),
+        "vc_token_logprobs")
 
 
 # ---------------------------------------------------------------------------

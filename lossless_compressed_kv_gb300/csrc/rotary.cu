@@ -102,6 +102,105 @@ __global__ void __launch_bounds__(256) rotary_pairs_kernel(const __grid_constant
     }
 }
 
+// Rows whose halves (or pairs) come in whole 16-byte pieces of the output: a
+// block takes a few rows; their angles' sines go to shared memory once for all
+// heads, then a thread takes 8 output channels (interleaved, or copied ones) or
+// two times 8 (both halves of 8 pairs) at a time, 16-byte stores.  Bound by
+// memory: each value is read once and written once.
+constexpr int kThreadsV = 256;
+
+template <typename T>
+__device__ inline void load8(const T *p, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+__device__ inline void store8(uint16_t *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+
+constexpr int kMaxRows = 16;
+template <typename T, bool INTER>
+__global__ void __launch_bounds__(kThreadsV) rotary_wide_kernel(const __grid_constant__ RotArgs a, int rows) {
+    pdl_begin();
+    extern __shared__ float2 cs[];  // [rows][half]
+    __shared__ int64_t base[kMaxRows];
+    const int r0 = blockIdx.x * rows, n = min(rows, a.m - r0);
+    if (threadIdx.x < n) base[threadIdx.x] = row_base(a, r0 + threadIdx.x);
+    for (int e = threadIdx.x; e < n * a.half; e += kThreadsV) {
+        const int k = e / a.half, i = e % a.half;
+        cs[e] = cos_sin(a.turns[i], a.pos[r0 + k], a.amp);
+    }
+    __syncthreads();
+    // items of a row: per head, `turned` pieces that rotate, then copied ones
+    const int turned = INTER ? a.half / 4 : a.half / 8, plain = (a.d - 2 * a.half) / 8, per = turned + plain;
+    const int items = (a.hq + 2 * a.hkv) * per;
+    for (int f = threadIdx.x; f < n * items; f += kThreadsV) {
+        const int k = f / items, e = f % items;
+        const int64_t kv = base[k];
+        if (kv < 0) continue;
+        const int h = e / per, i = e % per;
+        const T *x = reinterpret_cast<const T *>(a.qkv) + (int64_t)(r0 + k) * a.stride + h * a.d;
+        const float2 *c = cs + k * a.half;
+        uint16_t *dst = h < a.hq ? a.q + ((int64_t)(r0 + k) * a.hq + h) * a.d
+                        : h < a.hq + a.hkv ? a.kp + kv + (int64_t)(h - a.hq) * kPage * a.d
+                                           : a.vp + kv + (int64_t)(h - a.hq - a.hkv) * kPage * a.d;
+        const bool turn = h < a.hq + a.hkv;
+        float u[8];
+        if (i >= turned) {
+            const int ch = 2 * a.half + (i - turned) * 8;
+            load8(x + ch, u);
+            store8(dst + ch, u);
+        } else if (INTER) {
+            load8(x + i * 8, u);
+            if (turn) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float2 w = c[i * 4 + p];
+                    const float y0 = u[2 * p] * w.x - u[2 * p + 1] * w.y;
+                    u[2 * p + 1] = u[2 * p + 1] * w.x + u[2 * p] * w.y;
+                    u[2 * p] = y0;
+                }
+            }
+            store8(dst + i * 8, u);
+        } else {
+            float v[8];
+            load8(x + i * 8, u);
+            load8(x + a.half + i * 8, v);
+            if (turn) {
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const float2 w = c[i * 8 + p];
+                    const float y0 = u[p] * w.x - v[p] * w.y;
+                    v[p] = v[p] * w.x + u[p] * w.y;
+                    u[p] = y0;
+                }
+            }
+            store8(dst + i * 8, u);
+            store8(dst + a.half + i * 8, v);
+        }
+    }
+}
+
+template <typename T, bool INTER>
+cudaError_t launch_wide(const RotArgs &a, cudaStream_t st) {
+    // a row a block while there are few; else about four pieces a thread
+    const int items = (a.hq + 2 * a.hkv) * a.d / (INTER ? 8 : 16);
+    const int rows = a.m <= 1024 ? 1 : max(1, min(kMaxRows, 4 * kThreadsV / items));
+    return launch_pdl(rotary_wide_kernel<T, INTER>, ceil_div(a.m, rows), kThreadsV, rows * a.half * 8, st, a, rows);
+}
+
 // F_i of every pair, from 64-bit frequencies.
 void fill_turns(const vc_rotary &p, uint64_t *turns) {
     constexpr double kTwoPi = 6.283185307179586476925;
@@ -170,10 +269,18 @@ extern "C" vc_status vc_rotary_kv_write(const void *qkv, int32_t qkv_dtype, int6
     a.batch = full->batch;
     a.status = dev_status;
     fill_turns(*rotary, a.turns);
+    // 16-byte pieces: 8 channels of the output, of 8 pairs' halves or 4 pairs
+    const bool f32 = qkv_dtype == VC_F32;
+    const bool wide = a.half % (a.inter ? 4 : 8) == 0 && row_stride % (f32 ? 4 : 8) == 0 &&
+                      (((uintptr_t)qkv | (uintptr_t)q_out | (uintptr_t)a.kp | (uintptr_t)a.vp) & 15) == 0;
+    const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
-    if (qkv_dtype == VC_F32)
-        e = launch_pdl(rotary_pairs_kernel<float>, m, 256, 0, (cudaStream_t)stream, a);
+    if (wide)
+        e = f32 ? (a.inter ? launch_wide<float, true>(a, st) : launch_wide<float, false>(a, st))
+                : (a.inter ? launch_wide<uint16_t, true>(a, st) : launch_wide<uint16_t, false>(a, st));
+    else if (f32)
+        e = launch_pdl(rotary_pairs_kernel<float>, m, 256, 0, st, a);
     else
-        e = launch_pdl(rotary_pairs_kernel<uint16_t>, m, 256, 0, (cudaStream_t)stream, a);
+        e = launch_pdl(rotary_pairs_kernel<uint16_t>, m, 256, 0, st, a);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? VC_OK : VC_ERR_CUDA;
 }
