@@ -685,7 +685,8 @@ VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int
  *   y_v = (x_v - max x) / tau,  S = sum_v exp(y_v)
  *   log p_v = y_v - log S,  entropy = log S - sum_v y_v exp(y_v) / S
  *  logits        device, dtype VC_F32, VC_BF16 or VC_F16: row r at logits + r
- *                * row_stride values, vocab of them (row_stride >= vocab)
+ *                * row_stride values, vocab of them (vocab <= 2^22, row_stride >=
+ *                vocab)
  *  ids           device int32 [rows][n_ids], n_ids >= 0: the tokens asked for.
  *                -1 is no token (log probability 0); any other id outside [0,
  *                vocab) gets 0 too and is reported (VC_ERR_BAD_INDEX)

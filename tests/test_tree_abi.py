@@ -121,6 +121,7 @@ def test_logprobs_refuse_arguments(vc):
                 dict(tau=float("nan")), dict(tau=float("inf")), dict(k=-1), dict(x=None), dict(ids=None),
                 dict(lp=None), dict(ti=None), dict(tl=None)):
         assert call(**bad) == "VC_ERR_INVALID_ARG", bad
+    assert call(vocab=(1 << 22) + 1, stride=1 << 23) == "VC_ERR_UNSUPPORTED"
     assert call(dtype=3) == "VC_ERR_UNSUPPORTED" and call(k=65) == "VC_ERR_UNSUPPORTED"
     assert call(ws=None) == "VC_ERR_WORKSPACE" and call(nbytes=0) == "VC_ERR_WORKSPACE"
     assert call(rows=0, x=None, ids=None, lp=None, ws=None) == "VC_OK"
