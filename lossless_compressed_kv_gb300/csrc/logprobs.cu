@@ -20,8 +20,10 @@ struct Pack;
 template <>
 struct Pack<float> {
     static constexpr int VEC = 4;
+    using Word = uint32_t;
     static constexpr uint32_t kNone = 0xff800000u;  // words of -infinity
     __device__ static float one(const float *p) { return *p; }
+    __device__ static float of(Word w) { return __uint_as_float(w); }
     __device__ static void unpack(const uint4 &u, float (&v)[4]) {
         v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
         v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
@@ -45,8 +47,10 @@ __device__ inline float Pack<float>::max_of(const uint4 &u) {
 template <>
 struct Pack<__nv_bfloat16> {
     static constexpr int VEC = 8;
+    using Word = uint16_t;
     static constexpr uint32_t kNone = 0xff80ff80u;
     __device__ static float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    __device__ static float of(Word w) { return __uint_as_float((uint32_t)w << 16); }
     __device__ static void unpack(const uint4 &u, float (&v)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -67,8 +71,10 @@ struct Pack<__nv_bfloat16> {
 template <>
 struct Pack<__half> {
     static constexpr int VEC = 8;
+    using Word = uint16_t;
     static constexpr uint32_t kNone = 0xfc00fc00u;
     __device__ static float one(const __half *p) { return __half2float(*p); }
+    __device__ static float of(Word w) { return __half2float(__ushort_as_half(w)); }
     __device__ static void unpack(const uint4 &u, float (&v)[8]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -102,10 +108,10 @@ __device__ inline unsigned long long order_key(float v, int id) {
     return ((unsigned long long)order_bits(v) << 32) | (uint32_t)~(uint32_t)id;
 }
 // Two values in one packed instruction, each rounded as its scalar form.
-__device__ inline void sub_mul2(float &d0, float &d1, float a0, float a1, float b, float c) {  // (a - b) c
-    asm("{\n\t.reg .b64 ra, rb, rc;\n\t.reg .f32 nb;\n\tneg.f32 nb, %4;\n\t"
-        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {nb, nb};\n\tmov.b64 rc, {%5, %5};\n\t"
-        "add.rn.f32x2 ra, ra, rb;\n\tmul.rn.f32x2 ra, ra, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
+__device__ inline void fma2(float &d0, float &d1, float a0, float a1, float b, float c) {  // a b + c
+    asm("{\n\t.reg .b64 ra, rb, rc;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %4};\n\tmov.b64 rc, {%5, %5};\n\t"
+        "fma.rn.f32x2 ra, ra, rb, rc;\n\tmov.b64 {%0, %1}, ra;\n\t}"
         : "=f"(d0), "=f"(d1)
         : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
@@ -147,7 +153,8 @@ struct Stats {
 // one warp.  The first 32 tokens asked for and their logits come in registers.
 template <typename T>
 __device__ void finish_row(const LpArgs &a, int64_t row, Stats s, const unsigned long long *top, int have, int lane,
-                           int id, float logit) {
+                           int id, typename Pack<T>::Word raw) {
+    float logit = Pack<T>::of(raw);
     const bool none = s.m == -INFINITY, bad = s.m == INFINITY || s.m != s.m;
     const float nan = __int_as_float(0x7fffffff);
     const float log_s = none || bad ? 0.0f : logf(s.c) + log1pf(s.r / s.c);
@@ -171,82 +178,15 @@ __device__ void finish_row(const LpArgs &a, int64_t row, Stats s, const unsigned
             bad ? nan : in ? (order_value((uint32_t)(top[j] >> 32)) - s.m) * a.inv_tau - log_s : -INFINITY;
     }
 }
-// ... which this loads, early, so that the loads' latency is not met at the end.
-template <typename T>
-__device__ inline int asked(const LpArgs &a, int64_t row, int lane, float &logit) {
-    int id = -1;
-    logit = 0.0f;
-    if (lane < a.n_ids) {
-        id = a.ids[row * a.n_ids + lane];
-        if (id >= 0 && id < a.vocab) logit = Pack<T>::one(reinterpret_cast<const T *>(a.x) + row * a.stride + id);
-    }
-    return id;
+// ... which these load, early, so that the loads' latency is not met at the end.
+__device__ inline int asked_id(const LpArgs &a, int64_t row, int lane) {
+    return lane < a.n_ids ? a.ids[row * a.n_ids + lane] : -1;
 }
-
-// A part of a row in registers, NV packs a thread; pack j of thread t is pack
-// j * THREADS + t of the part (counted from the 16-byte boundary at or before
-// its first logit), so loads are whole and a run of neighbours is spread over
-// the threads.  Packs behind the part hold -infinity.
-template <typename T, int THREADS, int NV>
-struct Chunk {
-    using P = Pack<T>;
-    static constexpr int VEC = P::VEC;
-    uint4 x[NV];
-    int skew, packs;  // logits before the part in its first pack; packs
-
-    // place (in the part) of the first logit of this thread's pack j
-    __device__ int index(int j) const { return (j * THREADS + (int)threadIdx.x) * VEC - skew; }
-    __device__ bool holds(int j) const { return j * THREADS + (int)threadIdx.x < packs; }
-    __device__ void load(const T *p, int n) {
-        skew = (int)((uintptr_t)p & 15) / (int)sizeof(T);
-        packs = ceil_div(n + skew, VEC);
-        const uint4 *base = reinterpret_cast<const uint4 *>(p - skew) + threadIdx.x;
-        const uint4 none = make_uint4(P::kNone, P::kNone, P::kNone, P::kNone);
-        // whole packs: [first, last)
-        const int first = skew > 0, last = (n + skew) / VEC;
-        // an end within a pack: its logits one by one, -infinity beside them
-        auto edge = [&](int q) {
-            uint32_t w[4] = {P::kNone, P::kNone, P::kNone, P::kNone};
-#pragma unroll 1
-            for (int e = 0; e < VEC; ++e) {
-                const int i = q * VEC - skew + e;
-                if (i < 0 || i >= n) continue;
-                uint32_t bits, keep, at;
-                if constexpr (sizeof(T) == 4) {
-                    bits = reinterpret_cast<const uint32_t *>(p)[i];
-                    keep = 0;
-                    at = e;
-                } else {
-                    bits = (uint32_t) reinterpret_cast<const uint16_t *>(p)[i] << (16 * (e & 1));
-                    keep = e & 1 ? 0xffffu : 0xffff0000u;
-                    at = e >> 1;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (at == k) w[k] = (w[k] & keep) | bits;
-            }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        };
-        const bool cut = last < packs && last >= first;  // the last pack is not whole
-        uint4 head = none, end = none;
-        if (first && threadIdx.x == 0) head = edge(0);
-        if (cut && last % THREADS == threadIdx.x) end = edge(last);
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int q = j * THREADS + threadIdx.x;
-            if ((j > 0 || first == 0) && (j + 1) * THREADS <= last)  // whole for all threads
-                x[j] = __ldcs(base + j * THREADS);
-            else
-                x[j] = q >= first && q < last ? __ldcs(base + j * THREADS) : cut && q == last ? end : none;
-        }
-        if (first && threadIdx.x == 0) x[0] = head;
-    }
-    // The packs are read anew: what was unpacked of them is not kept in registers.
-    __device__ void again() {
-#pragma unroll
-        for (int j = 0; j < NV; ++j) asm volatile("" : "+r"(x[j].x), "+r"(x[j].y), "+r"(x[j].z), "+r"(x[j].w));
-    }
-};
+template <typename T>
+__device__ inline typename Pack<T>::Word asked_logit(const LpArgs &a, int64_t row, int id) {  // (as it lies in memory)
+    using W = typename Pack<T>::Word;
+    return id >= 0 && id < a.vocab ? reinterpret_cast<const W *>(a.x)[row * a.stride + id] : (W)0;
+}
 
 __device__ inline float warp_max_nan(float v) {
     float d;
@@ -263,18 +203,20 @@ __device__ inline float warp_sum2(float u, float v, int lane) {
     return s;
 }
 
-constexpr int kPacks = 256;  // packs with logits not below the bound that are kept (more: the row is read again)
-
-// A kernel's blocks: MAIN threads that go through the logits, NV packs each,
-// and one more warp that puts the alternatives in order and writes results.
-template <typename T, int MAIN_, int NV_, int MIN_CTAS_>
-struct Shape {
-    static constexpr int MAIN = MAIN_, NV = NV_, MIN_CTAS = MIN_CTAS_, THREADS = MAIN + 32, WARPS = MAIN / 32;
-    static constexpr int CANDS = MAIN >= 64 ? 2048 : 1024;  // logits not below the bound that are put in order
-    static constexpr int CAP = MAIN * NV * Pack<T>::VEC - (Pack<T>::VEC - 1);  // logits of a part, wherever it starts
-};
 __device__ inline void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ inline void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// Puts n keys in order, by one warp: each one's place is the number of larger ones.
+__device__ inline void order_keys(const unsigned long long *cand, int n, int k, unsigned long long *top, int lane) {
+    for (int i = lane; i < n; i += 32) {
+        const unsigned long long key = cand[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int q = 0; q < n; ++q) rank += cand[q] > key;
+        if (rank < k) top[rank] = key;
+    }
+    __syncwarp();
+}
 
 // The `have` largest keys of a part (at most k), in order, where too many
 // logits are not below the bound for the lists, by one warp that reads the part
@@ -294,12 +236,7 @@ __device__ int order_again(const T *x, int v0, int n, int k, float lo, unsigned 
     }
     __syncwarp();
     if (above <= cands) {
-        for (int i = lane; i < above; i += 32) {
-            const unsigned long long key = cand[i];
-            int rank = 0;
-            for (int q = 0; q < above; ++q) rank += cand[q] > key;
-            if (rank < k) top[rank] = key;
-        }
+        order_keys(cand, above, k, top, lane);
         int have = min(above, k);
         if (lo > -INFINITY)
             for (int i0 = 0; i0 < n && have < k; i0 += 32) {
@@ -347,251 +284,498 @@ __device__ inline Stats join_stats(Stats a, Stats b, float inv_tau) {
     return {a.m, a.c, a.r + f * (b.c + b.r), a.t + f * (b.t + d * (b.c + b.r))};
 }
 
-// One block per part of a row, in turn over the parts it owns.  The part stays
-// in registers; the main warps meet twice, for the maximum (and the groups'
-// maxima) and for the bound, and leave what is left to the last warp, which
-// finishes a part while they are at the next.  Memory bounds it at best (64 KB
-// of bf16 at an SM's share of the bandwidth take 1.4 us, 2600 cycles), with the
-// instructions close behind, so what comes next is asked into L2 before the
-// arithmetic begins, and the arithmetic is packed: maxima of 8 logits in 4
-// instructions, two logits' differences, products and sums in one; what the
-// maximum itself and -infinity need is done by the warps that meet them.
-template <typename T, typename S>
-__global__ void __launch_bounds__(S::THREADS, S::MIN_CTAS) logprobs_kernel(const __grid_constant__ LpArgs a) {
-    pdl_begin();
+// The sums of a thread's packs relative to `m`, every term added (the maximum's
+// too): r in units, t in units of log 2; those of packs that a thread holds.
+// y = scale (v - m) takes one multiply-add, scale v - h with h = scale m rounded:
+// every y is then too large by the same d = scale m - h, which is known and
+// comes off at the end (e^y by 2^-d, y e^y by d e^y as well).
+template <typename T, int NV>
+__device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float scale, float &r, float &t) {
     using P = Pack<T>;
-    constexpr int VEC = P::VEC, NV = S::NV, WARPS = S::WARPS;
-    constexpr int GROUPS = S::MAIN < 128 ? S::MAIN : 128;  // at most
-    // between the main warps (by turns where one may be at the next part already)
-    __shared__ float wmax[2][WARPS], bound_s[2];
-    __shared__ float gmax[GROUPS];
-    // from them to the last warp, by turns
-    struct Hand {
-        float m, lo, sum[2][WARPS];
-        int n_max, n_pack;
-        int at[kPacks];
-    };
-    __shared__ Hand hand[2];
-    __shared__ uint4 pack[2][kPacks];
-    // the last warp's own
-    __shared__ unsigned long long cand[S::CANDS], top[VC_MAX_TOP];
-    __shared__ int n_cand;
-    constexpr int kMain = 1, kReady = 2, kFree = 4;  // named barriers; the latter two by turns
+    constexpr int VEC = P::VEC;
+    float r2[2] = {0.0f, 0.0f}, t2[2] = {0.0f, 0.0f};
+    const float h = __fmul_rn(scale, m);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        if (j >= held) break;
+        float v[VEC];
+        P::unpack(x[j], v);
+#pragma unroll
+        for (int e = 0; e < VEC; e += 2) {
+            float y[2], p[2];
+            fma2(y[0], y[1], v[e], v[e + 1], scale, -h);
+            p[0] = ex2(y[0]);
+            p[1] = ex2(y[1]);
+            acc2(r2[0], r2[1], p[0], p[1]);
+            facc2(t2[0], t2[1], p[0], p[1], y[0], y[1]);
+        }
+    }
+    const float d = __fmaf_rn(scale, m, -h), f = ex2(-d);
+    r = r2[0] + r2[1];
+    t = f * __fmaf_rn(-d, r, t2[0] + t2[1]);
+    r *= f;
+}
+// The same where -infinity may be among them (0 times infinity above; here a
+// bound keeps it out of y e^y: e^y is 0 long before) or the maximum, which is
+// counted and not added.
+template <typename T>
+__device__ inline void careful_sums(uint4 u, float m, float scale, float &r, float &t, int &c) {
+    float v[Pack<T>::VEC];
+    Pack<T>::unpack(u, v);
+#pragma unroll
+    for (int e = 0; e < Pack<T>::VEC; ++e) {
+        const float y = fmaxf((v[e] - m) * scale, -10000.0f), p = ex2(y);
+        c += v[e] == m;
+        r += v[e] == m ? 0.0f : p;
+        t = fmaf(p, y, t);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Long rows: a block streams parts of rows through shared memory.
+//
+// A producer warp keeps STAGES parts under way (one bulk copy each, the ends of
+// a part that share a 16-byte piece with something else by single loads).  16
+// main warps go through a part once: a thread takes NV packs of 16 bytes, their
+// maximum, and the sums relative to that; the warp's sums relative to the warp's
+// maximum.  They never meet.  One of 4 finishing warps, in turn, joins the
+// warps' sums, goes again through the 1/16 that holds the maximum to count it
+// apart, takes the k-th largest of 32 or 64 groups' maxima as a bound (k logits
+// at least are not below it), collects the logits not below it from the
+// threads whose maximum is not, puts them in order and writes the results.
+// Bound by instructions and memory alike: 64 KB take an SM's share of the
+// bandwidth 1.4 us, and the main warps' 7 instructions a logit about as long.
+// ---------------------------------------------------------------------------
+constexpr int kMainWarps = 16, kMain = kMainWarps * 32, kFinishers = 4;
+constexpr int kRingThreads = kMain + 32 * (kFinishers + 1);
+constexpr int kRingCands = 512;  // logits not below the bound (more: the part is read again)
+
+struct Hand {  // from the main warps to a finisher
+    float m[kMainWarps], t[kMainWarps];
+    float r[kMainWarps], top[kMainWarps];  // r apart: of the threads whose maximum is the warp's
+    float tmax[kMain];
+};
+struct Meta {  // from the producer: packs of a part, and logits before it in the first
+    int packs, skew;
+};
+template <int NV>
+struct Ring {
+    static constexpr int STAGE = kMain * NV * 16, STAGES = NV >= 8 ? 3 : 8;
+    static constexpr int OFF_HAND = STAGE * STAGES;
+    static constexpr int OFF_CAND = OFF_HAND + kFinishers * (int)sizeof(Hand);
+    static constexpr int OFF_TOP = OFF_CAND + kFinishers * kRingCands * 8;
+    static constexpr int OFF_GRP = OFF_TOP + kFinishers * VC_MAX_TOP * 8;
+    static constexpr int OFF_LIST = OFF_GRP + kFinishers * 32 * 4;
+    static constexpr int OFF_COUNT = OFF_LIST + kFinishers * kMain * 2;
+    static constexpr int OFF_META = OFF_COUNT + kFinishers * 8;
+    static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(Meta);
+    static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
+};
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __grid_constant__ LpArgs a) {
+    pdl_wait();
+    using P = Pack<T>;
+    using R = Ring<NV>;
+    constexpr int VEC = P::VEC;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR), *empty = full + R::STAGES;
+    volatile Meta *meta = reinterpret_cast<volatile Meta *>(smem + R::OFF_META);  // (of a stage)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t items = (int64_t)a.rows * a.parts;
-    int turn = 0;
-    if (warp == WARPS) {
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
-            const int64_t row = a.parts == 1 ? item : item / a.parts;
-            const int v0 = (int)(item - row * a.parts) * a.part_len;
-            float logit = 0.0f;
-            int id = -1;
-            if (a.parts == 1) id = asked<T>(a, row, lane, logit);
-            if (lane == 0) n_cand = 0;
-            bar_sync(kReady + turn, S::THREADS);
-            const Hand &h = hand[turn];
-            Stats s{h.m, (float)h.n_max, 0.0f, 0.0f};
-            const bool sound = s.m > -INFINITY && s.m < INFINITY;
-            const float both =
-                warp_sum2(lane < WARPS ? h.sum[0][lane] : 0.0f, lane < WARPS ? h.sum[1][lane] : 0.0f, lane);
-            s.r = __shfl_sync(0xffffffffu, both, 0);
-            s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
-            int have = 0;
-            if (a.k > 0 && sound) {
-                const float lo = h.lo;
-                const int np = h.n_pack;
-                int n = S::CANDS + 1;
-                if (np <= kPacks) {
-                    for (int i = lane; i < np; i += 32) {
-                        float v[VEC];
-                        P::unpack(pack[turn][i], v);
-                        const int at_v = h.at[i];
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e)
-                            if (v[e] >= lo && v[e] > -INFINITY) {
-                                const int at = atomicAdd(&n_cand, 1);
-                                if (at < S::CANDS) cand[at] = order_key(v[e], at_v + e);
-                            }
-                    }
-                    __syncwarp();
-                    n = n_cand;
-                }
-                if (n <= S::CANDS) {
-                    // each one's place among them (their order in memory is left to chance, this is not)
-                    for (int i = lane; i < n; i += 32) {
-                        const unsigned long long key = cand[i];
-                        int rank = 0;
-                        for (int q = 0; q < n; ++q) rank += cand[q] > key;
-                        if (rank < a.k) top[rank] = key;
-                    }
-                    have = min(a.k, n);
-                } else {
-                    have = order_again<T>(reinterpret_cast<const T *>(a.x) + row * a.stride + v0, v0,
-                                          min(a.part_len, a.vocab - v0), a.k, lo, cand, S::CANDS, top, lane);
-                }
-                __syncwarp();
+    const float scale = a.inv_tau * kLog2e;
+    bool alive = true;
+    if (tid == 0) {
+        for (int i = 0; i < R::STAGES; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // part `item`: its first logit, how many, and those before it in its first pack
+    struct Part {
+        const T *p;
+        int64_t row;
+        int v0, n, skew, packs;
+    };
+    auto part_of = [&](int64_t item) {
+        Part q;
+        q.row = a.parts == 1 ? item : item / a.parts;
+        q.v0 = (int)(item - q.row * a.parts) * a.part_len;
+        q.p = reinterpret_cast<const T *>(a.x) + q.row * a.stride + q.v0;
+        q.n = min(a.part_len, a.vocab - q.v0);
+        q.skew = (int)((uintptr_t)q.p & 15) / (int)sizeof(T);
+        q.packs = ceil_div(q.n + q.skew, VEC);
+        return q;
+    };
+    int stage = 0, parity = 0;
+    auto step = [&]() {
+        if (++stage == R::STAGES) {
+            stage = 0;
+            parity ^= 1;
+        }
+    };
+    if (warp == kMainWarps + kFinishers) {
+        // ---- producer ----
+        int64_t sent = 0;
+        for (int64_t item = blockIdx.x; item < items && alive; item += gridDim.x, ++sent) {
+            const Part q = part_of(item);
+            if (sent >= R::STAGES)
+                alive = __all_sync(0xffffffffu, mbar_wait(&empty[stage], parity ^ 1, a.status, kWaitNs));
+            if (!alive) break;
+            uint8_t *dst = smem + stage * R::STAGE;
+            const int first = q.skew > 0, last = (q.n + q.skew) / VEC;  // whole packs: [first, last)
+            if (lane == 0 && last > first) {
+                const uint32_t bytes = (uint32_t)(last - first) * 16;
+                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[stage])),
+                             "r"(bytes)
+                             : "memory");
+                bulk_g2s(dst + first * 16, q.p - q.skew + first * VEC, bytes, &full[stage]);
             }
-            if (item + 2 * (int64_t)gridDim.x < items) bar_arrive(kFree + turn, S::THREADS);
-            if (a.parts == 1) {
-                finish_row<T>(a, row, s, top, have, lane, id, logit);
-            } else {
-                unsigned long long *w = a.ws + item * (3 + a.k);
-                if (lane == 0) {
-                    reinterpret_cast<float2 *>(w)[0] = make_float2(s.m, s.c);
-                    reinterpret_cast<float2 *>(w)[1] = make_float2(s.r, s.t);
-                    w[2] = have;
+            // packs that are not whole: their logits, -infinity beside them
+            for (int side = 0; side < 2; ++side) {
+                const int pk = side ? last : 0;
+                if (side ? !(last < q.packs && last >= first) : !first) continue;
+                if (lane < VEC) {
+                    const int i = pk * VEC - q.skew + lane;
+                    using W = typename P::Word;
+                    reinterpret_cast<W *>(dst + pk * 16)[lane] =
+                        i >= 0 && i < q.n ? reinterpret_cast<const W *>(q.p)[i] : (W)P::kNone;
                 }
-                for (int i = lane; i < have; i += 32) w[3 + i] = top[i];
             }
             __syncwarp();
+            if (lane == 0) {
+                meta[stage].packs = q.packs;
+                meta[stage].skew = q.skew;
+                mbar_arrive(&full[stage]);
+            }
+            step();
+        }
+        pdl_trigger();
+        // no copy may be under way when the block ends
+        for (int i = 0; i < R::STAGES && i < sent; ++i) {
+            const int64_t uses = (sent - 1 - i) / R::STAGES;  // copies into slot i before its last one
+            if (!mbar_wait(&full[i], uses & 1, a.status, kWaitNs)) break;
         }
         return;
     }
-    const float scale = a.inv_tau * kLog2e;
-    // groups of threads whose maxima bound the k-th largest logit: warps or equal
-    // parts of warps, as many as it takes for k groups
-    int per = 32;
-    while (per > 1 && S::MAIN / per < a.k && 2 * (S::MAIN / per) <= GROUPS) per >>= 1;
-    const int groups = S::MAIN / per;
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
-        const int64_t row = a.parts == 1 ? item : item / a.parts;
-        const int v0 = (int)(item - row * a.parts) * a.part_len;
-        Chunk<T, S::MAIN, NV> ch;
-        ch.load(reinterpret_cast<const T *>(a.x) + row * a.stride + v0, min(a.part_len, a.vocab - v0));
-        if (tid == 0) {
-            const int64_t ni = item + gridDim.x;
-            if (ni < items) {  // the next part: whole 16-byte pieces within it
-                const int64_t nr = a.parts == 1 ? ni : ni / a.parts;
-                const int nv0 = (int)(ni - nr * a.parts) * a.part_len;
-                const T *np = reinterpret_cast<const T *>(a.x) + nr * a.stride + nv0;
-                const uintptr_t lo = ((uintptr_t)np + 15) & ~(uintptr_t)15;
-                const uintptr_t hi = (uintptr_t)(np + min(a.part_len, a.vocab - nv0)) & ~(uintptr_t)15;
-                if (hi > lo)
-                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(lo), "r"((uint32_t)(hi - lo))
-                                 : "memory");
-            }
-        }
-        // the hand-over two parts ago has been read
-        if (item >= 2 * (int64_t)gridDim.x) bar_sync(kFree + turn, S::THREADS);
-        Hand &h = hand[turn];
-        if (tid == 0) {
-            h.n_pack = h.n_max = 0;
-            bound_s[turn] = -INFINITY;
-        }
-        // ---- maxima ----
-        float mine = -INFINITY;  // this thread's maximum
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            mine = max_nan(mine, P::max_of(ch.x[j]));
-        const float wm = warp_max_nan(mine);
-        if (lane == 0) wmax[turn][warp] = wm;
-        if (a.k > 1) {
-            float g = mine;
-            for (int o = 1; o < per; o <<= 1) g = max_nan(g, __shfl_xor_sync(0xffffffffu, g, o));
-            if (tid % per == 0) gmax[tid / per] = g;
-        }
-        bar_sync(kMain, S::MAIN);
-        const float m = warp_max_nan(lane < WARPS ? wmax[turn][lane] : -INFINITY);
-        const bool sound = m > -INFINITY && m < INFINITY;
-        // ---- the bound: the k-th largest of the groups' maxima (k logits at
-        // least are not below it; with fewer groups than k: none), by one warp ----
-        if (a.k > 1 && sound && warp == WARPS - 1)
-            for (int i = lane; i < groups; i += 32) {
-                const float own = gmax[i];
-                int rank = 0;
-                for (int q = 0; q < groups; ++q) {
-                    const float o = gmax[q];
-                    rank += o > own || (o == own && q < i);
-                }
-                if (rank == a.k - 1) bound_s[turn] = own;
-            }
-        // ---- sums ----
-        float r2[2] = {0.0f, 0.0f}, t2[2] = {0.0f, 0.0f};  // t in units of log 2
-        if (sound) {
-            bool careful = wm == m;  // a warp that holds the maximum
-            if (!careful) {
-                ch.again();
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    if (!ch.holds(j)) continue;
-                    float v[VEC];
-                    P::unpack(ch.x[j], v);
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 2) {
-                        float y[2], p[2];
-                        sub_mul2(y[0], y[1], v[e], v[e + 1], m, scale);
-                        p[0] = ex2(y[0]);
-                        p[1] = ex2(y[1]);
-                        acc2(r2[0], r2[1], p[0], p[1]);
-                        facc2(t2[0], t2[1], p[0], p[1], y[0], y[1]);
-                    }
-                }
-                careful = __any_sync(0xffffffffu, !(t2[0] + t2[1] <= 0.0f));  // -infinity: 0 times infinity
-            }
-            if (careful) {
-                r2[0] = r2[1] = t2[0] = t2[1] = 0.0f;
-                ch.again();
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    if (!ch.holds(j)) continue;
-                    float v[VEC], rv[2] = {0.0f, 0.0f}, tv[2] = {0.0f, 0.0f};
-                    P::unpack(ch.x[j], v);
-#pragma unroll
-                    for (int e = 0; e < VEC; e += 2) {
-                        float y[2], p[2];
-                        sub_mul2(y[0], y[1], v[e], v[e + 1], m, scale);
-                        p[0] = ex2(y[0]);
-                        p[1] = ex2(y[1]);
-                        acc2(rv[0], rv[1], p[0], p[1]);
-                        facc2(tv[0], tv[1], p[0], p[1], y[0], y[1]);
-                    }
-                    if (!(rv[0] + rv[1] < 1.0f && tv[0] + tv[1] <= 0.0f)) {
-                        // it may hold the maximum (a term of 1), which is counted
-                        // and not added, or -infinity, which the bound keeps out of
-                        // y e^y: e^y is 0 long before
-                        int c = 0;
-                        rv[0] = rv[1] = tv[0] = tv[1] = 0.0f;
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float y = fmaxf((v[e] - m) * scale, -10000.0f), p = ex2(y);
-                            c += v[e] == m;
-                            rv[0] += v[e] == m ? 0.0f : p;
-                            tv[0] = fmaf(p, y, tv[0]);
-                        }
-                        if (c) atomicAdd(&h.n_max, c);
-                    }
-                    acc2(r2[0], r2[1], rv[0], rv[1]);
-                    acc2(t2[0], t2[1], tv[0], tv[1]);
-                }
-            }
-        }
-        const float rt = warp_sum2(r2[0] + r2[1], t2[0] + t2[1], lane);
-        if ((lane & 15) == 0) h.sum[lane >> 4][warp] = rt;
-        // ---- packs with alternatives ----
-        float lo = m;
-        if (a.k > 1) {
-            bar_sync(kMain, S::MAIN);
-            lo = bound_s[turn];
-        }
-        if (a.k > 0 && sound && mine >= lo && mine > -INFINITY) {
-            ch.again();
+    if (warp < kMainWarps) {
+        // ---- main warps ----
+        int f = 0;
+        int64_t k = 0;
+        for (int64_t item = blockIdx.x; item < items; item += gridDim.x, ++k) {
+            const uint8_t *src = smem + stage * R::STAGE + tid * 16;
+            alive = alive && mbar_wait(&full[stage], parity, a.status, kWaitNs);
+            // packs of this thread
+            const int packs = alive ? meta[stage].packs : 0;
+            const int held = packs > tid ? min(NV, (packs - tid + kMain - 1) / kMain) : 0;
+            uint4 x[NV];
+            float mine = -INFINITY;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const float pm = P::max_of(ch.x[j]);
-                if (pm >= lo && pm > -INFINITY) {
-                    const int at = atomicAdd(&h.n_pack, 1);
-                    if (at < kPacks) {
-                        pack[turn][at] = ch.x[j];
-                        h.at[at] = v0 + ch.index(j);
+                if (j >= held) break;
+                x[j] = *reinterpret_cast<const uint4 *>(src + j * (kMain * 16));
+                mine = max_nan(mine, P::max_of(x[j]));
+            }
+            const float wm = warp_max_nan(mine);
+            float r = 0.0f, t = 0.0f;
+            if (mine > -INFINITY && mine < INFINITY && wm < INFINITY) {
+                sums_of<T, NV>(x, held, mine, scale, r, t);
+                if (!(t <= 0.0f)) {  // -infinity is among them
+                    int c = 0;
+                    r = t = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < NV; ++j)
+                        if (j < held) careful_sums<T>(x[j], mine, scale, r, t, c);
+                    r += (float)c;
+                }
+                const float d = fmaxf((mine - wm) * scale, -10000.0f), g = ex2(d);
+                t = g * fmaf(d, r, t);
+                r *= g;
+            }
+            const bool holds_top = mine == wm;
+            const unsigned tops = __ballot_sync(0xffffffffu, holds_top);
+            float r_top = r;
+            if (tops & (tops - 1)) {  // (several: rare)
+                r_top = holds_top ? r : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) r_top += __shfl_xor_sync(0xffffffffu, r_top, o);
+            }
+            const float rt = warp_sum2(holds_top ? 0.0f : r, t, lane);
+            // (the finisher has read what it was handed before)
+            if (k >= kFinishers) bar_sync(1 + kFinishers + f, kMain + 32);
+            Hand &h = reinterpret_cast<Hand *>(smem + R::OFF_HAND)[f];
+            h.tmax[tid] = mine;
+            if (holds_top) h.top[warp] = r_top;
+            if (lane == 0) {
+                h.m[warp] = wm;
+                h.r[warp] = rt;
+            }
+            if (lane == 16) h.t[warp] = rt;
+            bar_arrive(1 + f, kMain + 32);
+            f = f + 1 == kFinishers ? 0 : f + 1;
+            step();
+        }
+        return;
+    }
+    // ---- finishing warps ----
+    const int f = warp - kMainWarps;
+    const Hand &h = reinterpret_cast<const Hand *>(smem + R::OFF_HAND)[f];
+    unsigned long long *cand = reinterpret_cast<unsigned long long *>(smem + R::OFF_CAND) + f * kRingCands;
+    unsigned long long *top = reinterpret_cast<unsigned long long *>(smem + R::OFF_TOP) + f * VC_MAX_TOP;
+    float *grp = reinterpret_cast<float *>(smem + R::OFF_GRP) + f * 32;
+    int16_t *list = reinterpret_cast<int16_t *>(smem + R::OFF_LIST) + f * kMain;
+    int *count = reinterpret_cast<int *>(smem + R::OFF_COUNT) + f * 2;
+    stage = f % R::STAGES;
+    int id_next = -1;
+    if (a.parts == 1 && blockIdx.x + (int64_t)f * gridDim.x < items)
+        id_next = asked_id(a, blockIdx.x + (int64_t)f * gridDim.x, lane);
+    for (int64_t item = blockIdx.x + (int64_t)f * gridDim.x; item < items; item += (int64_t)kFinishers * gridDim.x) {
+        const Part q = part_of(item);
+        const uint8_t *src = smem + stage * R::STAGE;
+        const int id = id_next;
+        typename P::Word logit = 0;
+        if (a.parts == 1) {
+            logit = asked_logit<T>(a, q.row, id);
+            const int64_t later = item + (int64_t)kFinishers * gridDim.x;
+            id_next = later < items ? asked_id(a, later, lane) : -1;
+        }
+        bar_sync(1 + f, kMain + 32);
+        Stats s;
+        const float wm = lane < kMainWarps ? h.m[lane] : -INFINITY;
+        s.m = warp_max_nan(wm);
+        s.c = s.r = s.t = 0.0f;
+        const bool sound = s.m > -INFINITY && s.m < INFINITY;
+        int have = 0, n = 0;
+        float lo = s.m;
+        if (sound) {
+            float tm[kMainWarps];  // maxima of the threads w * 32 + lane
+#pragma unroll
+            for (int w = 0; w < kMainWarps; ++w) tm[w] = h.tmax[w * 32 + lane];
+            // the packs of `threads` listed threads, 32 at a time
+            auto for_packs = [&](int threads, auto fn) {
+                for (int i0 = 0; i0 < threads * NV; i0 += 32) {
+                    const int i = i0 + lane;
+                    int pk = i < threads * NV ? (i % NV) * kMain + list[i / NV] : -1;
+                    if (pk >= q.packs) pk = -1;
+                    fn(pk);
+                }
+                __syncwarp();
+            };
+            float r = 0.0f, t = 0.0f;
+            if (wm > -INFINITY) {
+                const float d = fmaxf((wm - s.m) * scale, -10000.0f), g = ex2(d);
+                const float all = h.r[lane] + h.top[lane];
+                t = g * fmaf(d, all, h.t[lane]);
+                r = wm == s.m ? h.r[lane] : g * all;
+            }
+            // the threads that hold the maximum (listed in order: sums must not
+            // depend on chance): their terms again, it counted apart
+            int c = 0, threads = 0;
+            float unused = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kMainWarps; ++w) {
+                const unsigned who = __ballot_sync(0xffffffffu, tm[w] == s.m);
+                if (!who) continue;
+                if (tm[w] == s.m) list[threads + __popc(who & ((1u << lane) - 1))] = (int16_t)(w * 32 + lane);
+                threads += __popc(who);
+            }
+            __syncwarp();
+            for_packs(threads, [&](int pk) {
+                if (pk >= 0) careful_sums<T>(*reinterpret_cast<const uint4 *>(src + pk * 16), s.m, scale, r, unused, c);
+            });
+            const float both = warp_sum2(r, t, lane);
+            s.r = __shfl_sync(0xffffffffu, both, 0);
+            s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
+            s.c = (float)__reduce_add_sync(0xffffffffu, c);
+            if (a.k > 1) {
+                // 32 groups of 16 threads, for a larger k 64 of 8 (two a lane): the
+                // smallest maximum that fewer than k exceed
+                float g[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int w = 0; w < kMainWarps; ++w) g[w & 1] = fmaxf(g[w & 1], tm[w]);
+                const bool two = a.k > 24;
+                if (!two) g[0] = fmaxf(g[0], g[1]);
+                int above[2] = {0, 0};
+                for (int w = 0; w <= (int)two; ++w) {
+                    grp[lane] = w ? g[1] : g[0];
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 o = *reinterpret_cast<const float4 *>(grp + i);
+                        above[0] += (o.x > g[0]) + (o.y > g[0]) + (o.z > g[0]) + (o.w > g[0]);
+                        if (two) above[1] += (o.x > g[1]) + (o.y > g[1]) + (o.z > g[1]) + (o.w > g[1]);
                     }
+                    __syncwarp();
+                }
+                float least = above[0] < a.k ? g[0] : INFINITY;
+                if (two && above[1] < a.k) least = fminf(least, g[1]);
+                lo = -warp_max_nan(-least);
+            }
+            if (a.k > 0) {
+                // the logits not below it (and not -infinity), from the threads whose
+                // maximum is not, in an order left to chance (what follows is not)
+                const float floor = fmaxf(lo, -3.402823466e38f);
+                if (lane == 0) count[0] = count[1] = 0;
+                __syncwarp();
+                uint32_t mine = 0;
+#pragma unroll
+                for (int w = 0; w < kMainWarps; ++w) mine |= tm[w] >= floor ? 1u << w : 0u;
+                if (mine)
+                    for (int at = atomicAdd(&count[0], __popc(mine)); mine; mine &= mine - 1, ++at)
+                        list[at] = (int16_t)((__ffs(mine) - 1) * 32 + lane);
+                __syncwarp();
+                for_packs(count[0], [&](int pk) {
+                    if (pk < 0) return;
+                    float v[VEC];
+                    P::unpack(*reinterpret_cast<const uint4 *>(src + pk * 16), v);
+                    uint32_t in = 0;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) in |= v[e] >= floor ? 1u << e : 0u;
+                    if (in)
+                        for (int at = atomicAdd(&count[1], __popc(in)); in && at < kRingCands; in &= in - 1, ++at) {
+                            const int e = __ffs(in) - 1;
+                            cand[at] = order_key(P::one(reinterpret_cast<const T *>(src + pk * 16) + e),
+                                                 q.v0 + pk * VEC + e - q.skew);
+                        }
+                });
+                n = count[1];
+            }
+        }
+        // stage and hand-over are free again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (item + (int64_t)kFinishers * gridDim.x < items) bar_arrive(1 + kFinishers + f, kMain + 32);
+        stage = (stage + kFinishers) % R::STAGES;
+        if (a.k > 0 && sound) {
+            if (n <= kRingCands) {
+                order_keys(cand, n, a.k, top, lane);
+                have = min(a.k, n);
+            } else {
+                have = order_again<T>(q.p, q.v0, q.n, a.k, lo, cand, kRingCands, top, lane);
+            }
+        }
+        if (a.parts == 1) {
+            finish_row<T>(a, q.row, s, top, have, lane, id, logit);
+        } else {
+            unsigned long long *w = a.ws + item * (3 + a.k);
+            if (lane == 0) {
+                reinterpret_cast<float2 *>(w)[0] = make_float2(s.m, s.c);
+                reinterpret_cast<float2 *>(w)[1] = make_float2(s.r, s.t);
+                w[2] = have;
+            }
+            for (int i = lane; i < have; i += 32) w[3 + i] = top[i];
+        }
+        __syncwarp();
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Short rows: a warp each, the row in registers (NV packs a lane).
+// ---------------------------------------------------------------------------
+constexpr int kShortWarps = 4, kShortPacks = 8, kShortCands = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const __grid_constant__ LpArgs a) {
+    pdl_begin();
+    using P = Pack<T>;
+    constexpr int VEC = P::VEC, NV = kShortPacks;
+    __shared__ unsigned long long cands[kShortWarps][kShortCands], tops[kShortWarps][VC_MAX_TOP];
+    __shared__ int counts[kShortWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned long long *cand = cands[warp], *top = tops[warp];
+    const float scale = a.inv_tau * kLog2e;
+    for (int64_t row = (int64_t)blockIdx.x * kShortWarps + warp; row < a.rows; row += (int64_t)gridDim.x * kShortWarps) {
+        const T *p = reinterpret_cast<const T *>(a.x) + row * a.stride;
+        const int skew = (int)((uintptr_t)p & 15) / (int)sizeof(T), n = a.vocab, packs = ceil_div(n + skew, VEC);
+        const int held = packs > lane ? min(NV, (packs - lane + 31) / 32) : 0;
+        uint4 x[NV];
+        float mine = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i0 = (j * 32 + lane) * VEC - skew;
+            if (i0 >= 0 && i0 + VEC <= n) {
+                x[j] = __ldcs(reinterpret_cast<const uint4 *>(p + i0));
+            } else {  // an end of the row, or behind it
+                uint32_t w[4] = {P::kNone, P::kNone, P::kNone, P::kNone};
+                if (j < held) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e)
+                        if (i0 + e >= 0 && i0 + e < n) {
+                            const uint32_t v = reinterpret_cast<const typename P::Word *>(p)[i0 + e];
+                            if constexpr (VEC == 4)
+                                w[e] = v;
+                            else
+                                w[e / 2] = e % 2 ? (w[e / 2] & 0xffffu) | v << 16 : (w[e / 2] & 0xffff0000u) | v;
+                        }
+                }
+                x[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        const int id = asked_id(a, row, lane);
+        const auto logit = asked_logit<T>(a, row, id);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) mine = max_nan(mine, P::max_of(x[j]));
+        Stats s{warp_max_nan(mine), 0.0f, 0.0f, 0.0f};
+        const bool sound = s.m > -INFINITY && s.m < INFINITY;
+        int have = 0;
+        if (sound) {
+            float r = 0.0f, t = 0.0f;
+            int c = 0;
+            if (mine < s.m) sums_of<T, NV>(x, held, s.m, scale, r, t);
+            if (mine == s.m || !(t <= 0.0f)) {
+                r = t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < NV; ++j)
+                    if (j < held) careful_sums<T>(x[j], s.m, scale, r, t, c);
+            }
+            __syncwarp();
+            const float both = warp_sum2(r, t, lane);
+            s.r = __shfl_sync(0xffffffffu, both, 0);
+            s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
+            s.c = (float)__reduce_add_sync(0xffffffffu, c);
+            if (a.k > 0) {
+                // the k-th largest of the lanes' maxima is a bound
+                float lo = s.m;
+                if (a.k > 1) {
+                    int rank = 0;
+                    for (int q = 0; q < 32; ++q) {
+                        const float o = __shfl_sync(0xffffffffu, mine, q);
+                        rank += o > mine || (o == mine && q < lane);
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, rank == a.k - 1);
+                    lo = hit ? __shfl_sync(0xffffffffu, mine, __ffs(hit) - 1) : -INFINITY;
+                }
+                if (lane == 0) counts[warp] = 0;
+                __syncwarp();
+                if (mine >= lo && mine > -INFINITY) {
+#pragma unroll
+                    for (int j = 0; j < NV; ++j) {
+                        const float pm = P::max_of(x[j]);
+                        if (!(pm >= lo && pm > -INFINITY)) continue;
+                        float v[VEC];
+                        P::unpack(x[j], v);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e)
+                            if (v[e] >= lo && v[e] > -INFINITY) {
+                                const int at = atomicAdd(&counts[warp], 1);
+                                if (at < kShortCands) cand[at] = order_key(v[e], (j * 32 + lane) * VEC - skew + e);
+                            }
+                    }
+                }
+                __syncwarp();
+                const int nc = counts[warp];
+                if (nc <= kShortCands) {
+                    order_keys(cand, nc, a.k, top, lane);
+                    have = min(a.k, nc);
+                } else {
+                    have = order_again<T>(p, 0, n, a.k, lo, cand, kShortCands, top, lane);
                 }
             }
         }
-        if (tid == 0) {
-            h.m = m;
-            h.lo = lo;
-        }
-        bar_arrive(kReady + turn, S::THREADS);
+        finish_row<T>(a, row, s, top, have, lane, id, logit);
+        __syncwarp();
     }
 }
 
@@ -627,46 +811,41 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
         }
         if (rank < a.k) top[rank] = key;
     }
-    float logit;
-    const int id = asked<T>(a, row, threadIdx.x & 31, logit);
+    const int id = asked_id(a, row, threadIdx.x & 31);
+    const auto logit = asked_logit<T>(a, row, id);
     __syncthreads();
     if (threadIdx.x < 32) finish_row<T>(a, row, s, top, min(n, a.k), threadIdx.x, id, logit);
 }
 
-// Parts of a row, of one size: what a block of the largest shape holds.
-template <typename T>
-struct Shapes {
-    static constexpr int F = sizeof(T) / 2;  // packs are half as long in fp32
-    using Tiny = Shape<T, 32, 4 * F + 1, 12>;
-    using Small = Shape<T, 96, 6 * F, 6>;
-    using Middle = Shape<T, 480, 5 * F, 2>;
-    using Large = Shape<T, 480, 9 * F, 2 / F>;
-};
-constexpr int kPartMax = Shapes<float>::Large::CAP < Shapes<__half>::Large::CAP ? Shapes<float>::Large::CAP
-                                                                                : Shapes<__half>::Large::CAP;
+// Parts of a row: packs of at most 64 KB, of one size, a multiple of 8 logits.
 constexpr int kVocabMax = 1 << 22;
-void split(int vocab, int &parts, int &len) {
-    parts = ceil_div(vocab, kPartMax / 8 * 8);
+void split(int vocab, int dtype, int &parts, int &len) {
+    const int most = (kMain * 8 - 1) * (dtype == VC_F32 ? 4 : 8) / 8 * 8;  // (wherever it starts in its first pack)
+    parts = ceil_div(vocab, most);
     len = parts == 1 ? vocab : ceil_div(ceil_div(vocab, parts), 8) * 8;
     parts = ceil_div(vocab, len);
 }
 
-template <typename T, typename S>
-cudaError_t launch_shape(const LpArgs &a, cudaStream_t st) {
-    // as many blocks as are resident at once
-    const int64_t items = (int64_t)a.rows * a.parts, most = (int64_t)152 * S::MIN_CTAS;
-    return launch_pdl(logprobs_kernel<T, S>, dim3((unsigned)(items < most ? items : most)), S::THREADS, 0, st, a);
+template <typename T, int NV>
+cudaError_t launch_ring(const LpArgs &a, cudaStream_t st) {
+    const cudaError_t e = set_smem_limit((const void *)logprobs_ring_kernel<T, NV>, Ring<NV>::SMEM);
+    if (e != cudaSuccess) return e;
+    const int64_t items = (int64_t)a.rows * a.parts;
+    return launch_pdl(logprobs_ring_kernel<T, NV>, dim3((unsigned)(items < 152 ? items : 152)), kRingThreads,
+                      Ring<NV>::SMEM, st, a);
 }
 
 template <typename T>
-cudaError_t launch(LpArgs a, cudaStream_t st) {
-    using H = Shapes<T>;
-    split(a.vocab, a.parts, a.part_len);
-    const int n = a.part_len;
-    cudaError_t e = n <= H::Tiny::CAP     ? launch_shape<T, typename H::Tiny>(a, st)
-                    : n <= H::Small::CAP  ? launch_shape<T, typename H::Small>(a, st)
-                    : n <= H::Middle::CAP ? launch_shape<T, typename H::Middle>(a, st)
-                                          : launch_shape<T, typename H::Large>(a, st);
+cudaError_t launch(LpArgs a, int dtype, cudaStream_t st) {
+    constexpr int VEC = Pack<T>::VEC;
+    split(a.vocab, dtype, a.parts, a.part_len);
+    const int packs = ceil_div(a.part_len + VEC - 1, VEC);  // wherever the row starts
+    if (packs <= 32 * kShortPacks) {
+        const int64_t blocks = ((int64_t)a.rows + kShortWarps - 1) / kShortWarps, most = 152 * 6;
+        return launch_pdl(logprobs_short_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), kShortWarps * 32, 0,
+                          st, a);
+    }
+    cudaError_t e = packs <= kMain * 2 ? launch_ring<T, 2>(a, st) : launch_ring<T, 8>(a, st);
     if (e == cudaSuccess && a.parts > 1) e = launch_pdl(logprobs_join_kernel<T>, a.rows, 128, 0, st, a);
     return e;
 }
@@ -681,7 +860,7 @@ extern "C" {
 size_t vc_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top_k) {
     if (rows < 0 || vocab < 1 || vocab > kVocabMax || top_k < 0 || top_k > VC_MAX_TOP) return 0;
     int parts, len;
-    split(vocab, parts, len);
+    split(vocab, VC_F32, parts, len);  // (fp32 logits take the most parts)
     return parts == 1 ? 8 : (size_t)rows * parts * (3 + top_k) * 8;
 }
 
@@ -715,9 +894,9 @@ vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int
     a.top_lp = top_logprobs;
     a.status = dev_status;
     const cudaStream_t st = (cudaStream_t)stream;
-    const cudaError_t e = dtype == VC_F32    ? launch<float>(a, st)
-                          : dtype == VC_BF16 ? launch<__nv_bfloat16>(a, st)
-                                             : launch<__half>(a, st);
+    const cudaError_t e = dtype == VC_F32    ? launch<float>(a, dtype, st)
+                          : dtype == VC_BF16 ? launch<__nv_bfloat16>(a, dtype, st)
+                                             : launch<__half>(a, dtype, st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? VC_OK : VC_ERR_CUDA;
 }
 
