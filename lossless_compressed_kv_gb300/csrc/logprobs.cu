@@ -334,9 +334,11 @@ __device__ inline void careful_sums(uint4 u, float m, float scale, float &r, flo
 // ---------------------------------------------------------------------------
 // Long rows: a block streams parts of rows through shared memory.
 //
-// A producer warp keeps STAGES parts under way (one bulk copy each, the ends of
-// a part that share a 16-byte piece with something else by single loads).  16
-// main warps go through a part once: a thread takes NV packs of 16 bytes, their
+// A producer warp keeps STAGES parts under way, one bulk copy of the whole packs
+// of 16 bytes each; the few logits at a part's ends that share a pack with
+// something else are the finisher's (padded with -infinity they would send two
+// main warps through the careful sums in every row: 4096 rows of 32001 bf16
+// logits 97 instead of 55 us).  16 main warps go through a part once: a thread takes NV packs of 16 bytes, their
 // maximum, and the sums relative to that; the warp's sums relative to the warp's
 // maximum.  They never meet.  One of 4 finishing warps, in turn, joins the
 // warps' sums, goes again through the 1/16 that holds the maximum to count it
@@ -355,9 +357,6 @@ struct Hand {  // from the main warps to a finisher
     float r[kMainWarps], top[kMainWarps];  // r apart: of the threads whose maximum is the warp's
     float tmax[kMain];
 };
-struct Meta {  // from the producer: packs of a part, and logits before it in the first
-    int packs, skew;
-};
 template <int NV>
 struct Ring {
     static constexpr int STAGE = kMain * NV * 16, STAGES = NV >= 8 ? 3 : 8;
@@ -368,7 +367,8 @@ struct Ring {
     static constexpr int OFF_LIST = OFF_GRP + kFinishers * 32 * 4;
     static constexpr int OFF_COUNT = OFF_LIST + kFinishers * kMain * 2;
     static constexpr int OFF_META = OFF_COUNT + kFinishers * 8;
-    static constexpr int OFF_BAR = OFF_META + STAGES * (int)sizeof(Meta);
+    static constexpr int OFF_BAR = OFF_META + 64;
+    static_assert(STAGES * 4 <= 64, "packs of a stage");
     static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
 };
 
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
     constexpr int VEC = P::VEC;
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR), *empty = full + R::STAGES;
-    volatile Meta *meta = reinterpret_cast<volatile Meta *>(smem + R::OFF_META);  // (of a stage)
+    int *packs_of = reinterpret_cast<int *>(smem + R::OFF_META);  // of a stage
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t items = (int64_t)a.rows * a.parts;
     const float scale = a.inv_tau * kLog2e;
@@ -393,11 +393,12 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
         fence_mbar_init();
     }
     __syncthreads();
-    // part `item`: its first logit, how many, and those before it in its first pack
+    // part `item`: its first logit, its place in the row, how many; the logits
+    // before its first whole pack, and the whole packs
     struct Part {
         const T *p;
         int64_t row;
-        int v0, n, skew, packs;
+        int v0, n, head, packs;
     };
     auto part_of = [&](int64_t item) {
         Part q;
@@ -405,8 +406,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
         q.v0 = (int)(item - q.row * a.parts) * a.part_len;
         q.p = reinterpret_cast<const T *>(a.x) + q.row * a.stride + q.v0;
         q.n = min(a.part_len, a.vocab - q.v0);
-        q.skew = (int)((uintptr_t)q.p & 15) / (int)sizeof(T);
-        q.packs = ceil_div(q.n + q.skew, VEC);
+        const int skew = (int)((uintptr_t)q.p & 15) / (int)sizeof(T);
+        q.head = min(q.n, skew ? VEC - skew : 0);
+        q.packs = (q.n - q.head) / VEC;
         return q;
     };
     int stage = 0, parity = 0;
@@ -424,31 +426,14 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             if (sent >= R::STAGES)
                 alive = __all_sync(0xffffffffu, mbar_wait(&empty[stage], parity ^ 1, a.status, kWaitNs));
             if (!alive) break;
-            uint8_t *dst = smem + stage * R::STAGE;
-            const int first = q.skew > 0, last = (q.n + q.skew) / VEC;  // whole packs: [first, last)
-            if (lane == 0 && last > first) {
-                const uint32_t bytes = (uint32_t)(last - first) * 16;
-                asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[stage])),
-                             "r"(bytes)
-                             : "memory");
-                bulk_g2s(dst + first * 16, q.p - q.skew + first * VEC, bytes, &full[stage]);
-            }
-            // packs that are not whole: their logits, -infinity beside them
-            for (int side = 0; side < 2; ++side) {
-                const int pk = side ? last : 0;
-                if (side ? !(last < q.packs && last >= first) : !first) continue;
-                if (lane < VEC) {
-                    const int i = pk * VEC - q.skew + lane;
-                    using W = typename P::Word;
-                    reinterpret_cast<W *>(dst + pk * 16)[lane] =
-                        i >= 0 && i < q.n ? reinterpret_cast<const W *>(q.p)[i] : (W)P::kNone;
-                }
-            }
-            __syncwarp();
             if (lane == 0) {
-                meta[stage].packs = q.packs;
-                meta[stage].skew = q.skew;
-                mbar_arrive(&full[stage]);
+                *(volatile int *)&packs_of[stage] = q.packs;
+                if (q.packs > 0) {
+                    mbar_arrive_expect_tx(&full[stage], q.packs * 16);
+                    bulk_g2s(smem + stage * R::STAGE, q.p + q.head, q.packs * 16, &full[stage]);
+                } else {
+                    mbar_arrive(&full[stage]);
+                }
             }
             step();
         }
@@ -468,7 +453,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             const uint8_t *src = smem + stage * R::STAGE + tid * 16;
             alive = alive && mbar_wait(&full[stage], parity, a.status, kWaitNs);
             // packs of this thread
-            const int packs = alive ? meta[stage].packs : 0;
+            const int packs = alive ? *(volatile int *)&packs_of[stage] : 0;
             const int held = packs > tid ? min(NV, (packs - tid + kMain - 1) / kMain) : 0;
             uint4 x[NV];
             float mine = -INFINITY;
@@ -541,10 +526,16 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             const int64_t later = item + (int64_t)kFinishers * gridDim.x;
             id_next = later < items ? asked_id(a, later, lane) : -1;
         }
+        // a logit at an end of the part, beside the whole packs (at most 14)
+        const int loose_i = lane < q.head ? lane : lane >= 8 && lane < 16 ? q.head + q.packs * VEC + lane - 8 : -1;
+        typename P::Word loose_w = 0;
+        const bool has_loose = loose_i >= 0 && loose_i < q.n;
+        if (has_loose) loose_w = reinterpret_cast<const typename P::Word *>(q.p)[loose_i];
         bar_sync(1 + f, kMain + 32);
+        const float loose = has_loose ? P::of(loose_w) : -INFINITY;
         Stats s;
         const float wm = lane < kMainWarps ? h.m[lane] : -INFINITY;
-        s.m = warp_max_nan(wm);
+        s.m = warp_max_nan(max_nan(wm, loose));
         s.c = s.r = s.t = 0.0f;
         const bool sound = s.m > -INFINITY && s.m < INFINITY;
         int have = 0, n = 0;
@@ -572,8 +563,13 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             }
             // the threads that hold the maximum (listed in order: sums must not
             // depend on chance): their terms again, it counted apart
-            int c = 0, threads = 0;
+            int c = loose == s.m, threads = 0;
             float unused = 0.0f;
+            if (loose > -INFINITY && loose < s.m) {
+                const float y = fmaxf((loose - s.m) * scale, -10000.0f), p = ex2(y);
+                r += p;
+                t = fmaf(p, y, t);
+            }
 #pragma unroll
             for (int w = 0; w < kMainWarps; ++w) {
                 const unsigned who = __ballot_sync(0xffffffffu, tm[w] == s.m);
@@ -619,6 +615,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 const float floor = fmaxf(lo, -3.402823466e38f);
                 if (lane == 0) count[0] = count[1] = 0;
                 __syncwarp();
+                if (loose >= floor) {
+                    const int at = atomicAdd(&count[1], 1);  // (the first: there is room)
+                    cand[at] = order_key(loose, q.v0 + loose_i);
+                }
                 uint32_t mine = 0;
 #pragma unroll
                 for (int w = 0; w < kMainWarps; ++w) mine |= tm[w] >= floor ? 1u << w : 0u;
@@ -626,20 +626,33 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                     for (int at = atomicAdd(&count[0], __popc(mine)); mine; mine &= mine - 1, ++at)
                         list[at] = (int16_t)((__ffs(mine) - 1) * 32 + lane);
                 __syncwarp();
-                for_packs(count[0], [&](int pk) {
-                    if (pk < 0) return;
-                    float v[VEC];
-                    P::unpack(*reinterpret_cast<const uint4 *>(src + pk * 16), v);
+                // four packs a lane at a time: which of their logits, then one count
+                // for all of them (most lanes have none)
+                const int packs = count[0] * NV;
+                for (int i0 = lane; i0 < packs; i0 += 128) {
+                    auto pack_of = [&](int k) {
+                        const int i = i0 + 32 * k;
+                        const int pk = i < packs ? (i % NV) * kMain + list[i / NV] : q.packs;
+                        return pk < q.packs ? pk : -1;
+                    };
                     uint32_t in = 0;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) in |= v[e] >= floor ? 1u << e : 0u;
+                    for (int k = 0; k < 4; ++k) {
+                        const int pk = pack_of(k);
+                        if (pk < 0) continue;
+                        float v[VEC];
+                        P::unpack(*reinterpret_cast<const uint4 *>(src + pk * 16), v);
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) in |= v[e] >= floor ? 1u << (8 * k + e) : 0u;
+                    }
                     if (in)
                         for (int at = atomicAdd(&count[1], __popc(in)); in && at < kRingCands; in &= in - 1, ++at) {
-                            const int e = __ffs(in) - 1;
+                            const int bit = __ffs(in) - 1, pk = pack_of(bit / 8), e = bit % 8;
                             cand[at] = order_key(P::one(reinterpret_cast<const T *>(src + pk * 16) + e),
-                                                 q.v0 + pk * VEC + e - q.skew);
+                                                 q.v0 + q.head + pk * VEC + e);
                         }
-                });
+                }
+                __syncwarp();
                 n = count[1];
             }
         }
@@ -677,7 +690,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
 constexpr int kShortWarps = 4, kShortPacks = 8, kShortCands = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const __grid_constant__ LpArgs a) {
+__global__ void __launch_bounds__(kShortWarps * 32, 8) logprobs_short_kernel(const __grid_constant__ LpArgs a) {
     pdl_begin();
     using P = Pack<T>;
     constexpr int VEC = P::VEC, NV = kShortPacks;
@@ -686,7 +699,10 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     unsigned long long *cand = cands[warp], *top = tops[warp];
     const float scale = a.inv_tau * kLog2e;
-    for (int64_t row = (int64_t)blockIdx.x * kShortWarps + warp; row < a.rows; row += (int64_t)gridDim.x * kShortWarps) {
+    const int64_t step = (int64_t)gridDim.x * kShortWarps;
+    int64_t row = (int64_t)blockIdx.x * kShortWarps + warp;
+    int id_next = row < a.rows ? asked_id(a, row, lane) : -1;
+    for (; row < a.rows; row += step) {
         const T *p = reinterpret_cast<const T *>(a.x) + row * a.stride;
         const int skew = (int)((uintptr_t)p & 15) / (int)sizeof(T), n = a.vocab, packs = ceil_div(n + skew, VEC);
         const int held = packs > lane ? min(NV, (packs - lane + 31) / 32) : 0;
@@ -713,8 +729,13 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
                 x[j] = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        const int id = asked_id(a, row, lane);
+        const int id = id_next;
         const auto logit = asked_logit<T>(a, row, id);
+        if (row + step < a.rows) {  // what comes next: its tokens, and its logits into L2
+            id_next = asked_id(a, row + step, lane);
+            const int64_t ahead = (int64_t)lane * 128 / (int)sizeof(T);
+            if (ahead < n) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + step * a.stride + ahead));
+        }
 #pragma unroll
         for (int j = 0; j < NV; ++j) mine = max_nan(mine, P::max_of(x[j]));
         Stats s{warp_max_nan(mine), 0.0f, 0.0f, 0.0f};
@@ -780,6 +801,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
 }
 
 // Rows of several parts: one block joins a row's statistics and alternatives.
+constexpr int kJoinKeys = 1024;
 template <typename T>
 __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constant__ LpArgs a) {
     pdl_begin();
@@ -798,18 +820,37 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
         n += (int)w[p * size + 2];
     }
     if (nan) s.m = __int_as_float(0x7fffffff);
-    // a key's place: its place in its own part, and the larger ones of the others
-    for (int i = threadIdx.x; i < a.parts * a.k; i += blockDim.x) {
-        const int p = i / a.k, j = i % a.k;
-        if (j >= (int)w[p * size + 2]) continue;
-        const unsigned long long key = w[p * size + 3 + j];
-        int rank = j;
-        for (int o = 0; o < a.parts; ++o) {
-            if (o == p) continue;
-            const int no = (int)w[o * size + 2];
-            for (int q = 0; q < no && w[o * size + 3 + q] > key; ++q) ++rank;
+    // a key's place is the number of larger ones: among all of them in shared
+    // memory, or, where they are many, its place in its own part and the larger
+    // ones of the others
+    __shared__ unsigned long long keys[kJoinKeys];
+    const int all = a.parts * a.k;
+    if (all <= kJoinKeys) {
+        for (int i = threadIdx.x; i < all; i += blockDim.x) {
+            const int p = i / a.k, j = i % a.k;
+            keys[i] = j < (int)w[p * size + 2] ? w[p * size + 3 + j] : 0;
         }
-        if (rank < a.k) top[rank] = key;
+        __syncthreads();
+        for (int i = threadIdx.x; i < all; i += blockDim.x) {
+            const unsigned long long key = keys[i];
+            int rank = 0;
+#pragma unroll 8
+            for (int q = 0; q < all; ++q) rank += keys[q] > key;
+            if (key && rank < a.k) top[rank] = key;
+        }
+    } else {
+        for (int i = threadIdx.x; i < all; i += blockDim.x) {
+            const int p = i / a.k, j = i % a.k;
+            if (j >= (int)w[p * size + 2]) continue;
+            const unsigned long long key = w[p * size + 3 + j];
+            int rank = j;
+            for (int o = 0; o < a.parts; ++o) {
+                if (o == p) continue;
+                const int no = (int)w[o * size + 2];
+                for (int q = 0; q < no && w[o * size + 3 + q] > key; ++q) ++rank;
+            }
+            if (rank < a.k) top[rank] = key;
+        }
     }
     const int id = asked_id(a, row, threadIdx.x & 31);
     const auto logit = asked_logit<T>(a, row, id);
@@ -841,7 +882,7 @@ cudaError_t launch(LpArgs a, int dtype, cudaStream_t st) {
     split(a.vocab, dtype, a.parts, a.part_len);
     const int packs = ceil_div(a.part_len + VEC - 1, VEC);  // wherever the row starts
     if (packs <= 32 * kShortPacks) {
-        const int64_t blocks = ((int64_t)a.rows + kShortWarps - 1) / kShortWarps, most = 152 * 6;
+        const int64_t blocks = ((int64_t)a.rows + kShortWarps - 1) / kShortWarps, most = 152 * 8;
         return launch_pdl(logprobs_short_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), kShortWarps * 32, 0,
                           st, a);
     }

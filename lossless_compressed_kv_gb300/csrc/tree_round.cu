@@ -90,8 +90,8 @@ struct CommitArgs {
 };
 
 // One block per (request, layer).  Each thread moves one 16-byte piece of
-// every entry, in path order: a target is below its source and the sources
-// ascend, so no later source has been written.
+// every entry, in path order, four loads under way at a time: a target is not
+// above its source and the sources ascend, so no target is a later source.
 __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant__ CommitArgs a) {
     pdl_begin();
     __shared__ int64_t src[kNodes], dst[kNodes];  // 16-byte pieces from the pool's start, kv head 0
@@ -130,8 +130,15 @@ __global__ void __launch_bounds__(256) tree_commit_kernel(const __grid_constant_
         uint4 *pool = a.pool[blockIdx.y][e >= items / 2];
         const int r = e % (items / 2);
         const int64_t off = (int64_t)(r / a.chunks) * kPage * a.chunks + r % a.chunks;
-        for (int j = 1; j <= len; ++j)
-            if (src[j] != dst[j]) pool[dst[j] + off] = pool[src[j] + off];
+        for (int j0 = 1; j0 <= len; j0 += 4) {
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j0 + k <= len && src[j0 + k] != dst[j0 + k]) u[k] = pool[src[j0 + k] + off];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (j0 + k <= len && src[j0 + k] != dst[j0 + k]) pool[dst[j0 + k] + off] = u[k];
+        }
     }
 }
 
