@@ -262,22 +262,20 @@ __device__ inline float max_of(const float (&v)[N]) {
     return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// 16 bytes of bf16 without their infinities and NaN (set to 0); whether there were any.
+// Which of two bf16 values are infinite or NaN (the exponent all ones: 1 more
+// carries into the sign's place): bits 15 and 31.
+__device__ inline uint32_t non_finite(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// 16 bytes of bf16 without them (set to 0); whether there were any.
 __device__ inline bool clear_non_finite(uint4 &u) {
-    bool any = false;
+    if (!(non_finite(u.x) | non_finite(u.y) | non_finite(u.z) | non_finite(u.w))) return false;
     uint32_t *w = reinterpret_cast<uint32_t *>(&u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if ((w[i] & 0x7f80u) == 0x7f80u) {
-            w[i] &= 0xffff0000u;
-            any = true;
-        }
-        if ((w[i] & 0x7f800000u) == 0x7f800000u) {
-            w[i] &= 0x0000ffffu;
-            any = true;
-        }
+        const uint32_t f = non_finite(w[i]);
+        if (f & 0x8000u) w[i] &= 0xffff0000u;
+        if (f & 0x80000000u) w[i] &= 0x0000ffffu;
     }
-    return any;
+    return true;
 }
 
 // Row rg's bits of the block of keys [key0, key0 + 64): which of them count.
@@ -471,6 +469,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                     }
                     copy(i, cur, &a.kmap, false);
                     if (alive) copy(i, cur, &a.vmap, true);
+                    // the last segment's end, now that its copy has had the time of
+                    // this one's first
+                    if (pending && pend.seg != seg) flush();
                 }
                 ++seg;
             }
@@ -565,13 +566,12 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             const int64_t orow = ((int64_t)w.seg_b * a.n_q + qi) * a.hq + (int64_t)w.seg_kvh * a.grp + qn;
             unsigned long long mask = 0;
             if (alive) {
-                // this row of Q, to TMEM as bf16 pairs or to shared memory
-                uint4 u[D / 8];
-                const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) u[j] = rvalid ? src[j] : make_uint4(0, 0, 0, 0);
                 if (rvalid) mask = a.mask[(int64_t)w.seg_b * a.n_q + qi] & (~0ull >> (64 - a.n_q));
-                if constexpr (C::QTM) {
+                if constexpr (C::QTM) {  // this row of Q, to TMEM as bf16 pairs
+                    uint4 u[D / 8];
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) u[j] = rvalid ? src[j] : make_uint4(0, 0, 0, 0);
 #pragma unroll
                     for (int c0 = 0; c0 < D / 2; c0 += 16) {
                         float v[16];
@@ -585,10 +585,19 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                         vtc::tmem_st16_nowait(tmem + lane_base + C::Q_COL0 + c0, v);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                } else {
+                } else {  // the warp's rows, to shared memory: a row's pieces by neighbouring lanes
+                    constexpr int L = D / 8, RPI = 32 / L;  // lanes a row, rows at a time
+                    uint4 u[L];
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j)
-                        *reinterpret_cast<uint4 *>(sq + t * C::QTILE + vtc::sw128(r, j, kTileRows)) = u[j];
+                    for (int i = 0; i < L; ++i) {
+                        const int rr = i * RPI + lane / L;
+                        const int64_t ro = __shfl_sync(0xffffffffu, rvalid ? orow : (int64_t)-1, rr);
+                        u[i] = ro >= 0 ? reinterpret_cast<const uint4 *>(a.q + ro * D)[lane % L] : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < L; ++i)
+                        *reinterpret_cast<uint4 *>(sq + t * C::QTILE + vtc::sw128((warp & 3) * 32 + i * RPI + lane / L,
+                                                                                  lane % L, kTileRows)) = u[i];
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 vtc::tc_fence_before();
