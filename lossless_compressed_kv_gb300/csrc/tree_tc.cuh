@@ -81,10 +81,14 @@ struct Cfg {
     static constexpr bool QTM = QT == 1;     // Q in TMEM
     static constexpr int QTILE = kTileRows * D * 2;
     static constexpr int OFF_KV = QTM ? 0 : QT * QTILE;
-    static constexpr int FIT = ((QT == 1 ? 110 : 224) * 1024 - OFF_KV) / SLOT;
+    // where a softmax warp turns rows round (32 rows x 128 bytes each); with Q
+    // in shared memory the warp's own rows of Q, which are done with by then
+    static constexpr int STAGE = QTM ? 4 * 4096 : 0;
+    static constexpr int FIT = ((QT == 1 ? 113 : 225) * 1024 - 512 - OFF_KV - STAGE) / SLOT;
     static constexpr int SLOTS = FIT < 14 ? FIT : 14;
     static_assert(SLOTS >= 5 && SLOTS / 2 + 2 <= kBadRing, "ring depth");
-    static constexpr int OFF_BAR = OFF_KV + SLOTS * SLOT;
+    static constexpr int OFF_STAGE = OFF_KV + SLOTS * SLOT;
+    static constexpr int OFF_BAR = OFF_STAGE + STAGE;
     static constexpr int NBAR = 4 * QT + 2 * SLOTS + 1;  // q, s, p, o per tile; full, empty; tail
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 16;
@@ -284,29 +288,6 @@ __device__ inline unsigned long long seen_bits(unsigned long long mask, int key0
     if (sh <= -64) return ~0ull;
     if (sh < 0) return (mask << -sh) | ((1ull << -sh) - 1);
     return sh >= 64 ? 0ull : mask >> sh;
-}
-
-// One row's result: the final value of a finished unit, in out's type.
-__device__ inline void store_ws8(float *dst, const float *v) {  // 32 bytes, one sector
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-}
-template <int D>
-__device__ inline void store_out16(const Args &a, int64_t orow, int c0, const float (&v)[16], float f, bool zero) {
-    float y[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = zero ? 0.0f : v[i] * f;
-    if (a.out_bf16) {
-        uint4 *dst = reinterpret_cast<uint4 *>((uint16_t *)a.out + orow * D + c0);
-        dst[0] = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        dst[1] = make_uint4(pack_bf16(y[8], y[9]), pack_bf16(y[10], y[11]), pack_bf16(y[12], y[13]),
-                            pack_bf16(y[14], y[15]));
-    } else {
-        float4 *dst = reinterpret_cast<float4 *>((float *)a.out + orow * D + c0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-    }
 }
 
 template <int D, int QT>
@@ -560,6 +541,13 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
         const int rg = (tile0 + t) * kTileRows + r;
         const bool rvalid = rg < a.n_q * a.grp;
         const int qi = rvalid ? rg / a.grp : 0, qn = rvalid ? rg % a.grp : 0;
+        // the warp's 32 rows x 8 pieces of 16 bytes, on their way between a
+        // thread's own row and eight neighbouring lanes a row (whole lines of
+        // global memory; a thread by itself would touch 32 of them at a time)
+        uint4 *stage = reinterpret_cast<uint4 *>(C::QTM ? smem + C::OFF_STAGE + warp * 4096
+                                                        : sq + t * C::QTILE + (warp & 3) * 4096);
+        const int srow = lane >> 3, spc = lane & 7;  // row (of 4 at a time) and piece
+        auto at = [&](int row, int piece) { return stage + row * 8 + (piece ^ (row & 7)); };
         uint32_t it = 0, seg = 0;  // blocks and segments of this chain
         for (; w.next(a); ++seg) {
             const int base = w.seg_len - a.n_q;
@@ -567,39 +555,40 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             unsigned long long mask = 0;
             if (alive) {
                 if (rvalid) mask = a.mask[(int64_t)w.seg_b * a.n_q + qi] & (~0ull >> (64 - a.n_q));
-                if constexpr (C::QTM) {  // this row of Q, to TMEM as bf16 pairs
-                    uint4 u[D / 8];
-                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + orow * D);
+                // the warp's rows of Q, 64 channels at a time
+                uint4 u[D / 64][8];
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j) u[j] = rvalid ? src[j] : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t ro = __shfl_sync(0xffffffffu, rvalid ? orow : (int64_t)-1, i * 4 + srow);
+                    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ro * D) + spc;
 #pragma unroll
-                    for (int c0 = 0; c0 < D / 2; c0 += 16) {
-                        float v[16];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            v[4 * j] = __uint_as_float(u[c0 / 4 + j].x);
-                            v[4 * j + 1] = __uint_as_float(u[c0 / 4 + j].y);
-                            v[4 * j + 2] = __uint_as_float(u[c0 / 4 + j].z);
-                            v[4 * j + 3] = __uint_as_float(u[c0 / 4 + j].w);
-                        }
-                        vtc::tmem_st16_nowait(tmem + lane_base + C::Q_COL0 + c0, v);
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                } else {  // the warp's rows, to shared memory: a row's pieces by neighbouring lanes
-                    constexpr int L = D / 8, RPI = 32 / L;  // lanes a row, rows at a time
-                    uint4 u[L];
-#pragma unroll
-                    for (int i = 0; i < L; ++i) {
-                        const int rr = i * RPI + lane / L;
-                        const int64_t ro = __shfl_sync(0xffffffffu, rvalid ? orow : (int64_t)-1, rr);
-                        u[i] = ro >= 0 ? reinterpret_cast<const uint4 *>(a.q + ro * D)[lane % L] : make_uint4(0, 0, 0, 0);
-                    }
-#pragma unroll
-                    for (int i = 0; i < L; ++i)
-                        *reinterpret_cast<uint4 *>(sq + t * C::QTILE + vtc::sw128((warp & 3) * 32 + i * RPI + lane / L,
-                                                                                  lane % L, kTileRows)) = u[i];
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    for (int h = 0; h < D / 64; ++h) u[h][i] = ro >= 0 ? src[h * 8] : make_uint4(0, 0, 0, 0);
                 }
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) {
+                    if constexpr (C::QTM) {  // to TMEM, bf16 pairs
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) *at(i * 4 + srow, spc) = u[h][i];
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            float v[16];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(v + 4 * j) = *at(lane, c * 4 + j);
+                            vtc::tmem_st16_nowait(tmem + lane_base + C::Q_COL0 + h * 32 + c * 16, v);
+                        }
+                        __syncwarp();
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<uint4 *>(
+                                sq + t * C::QTILE + vtc::sw128((warp & 3) * 32 + i * 4 + srow, h * 8 + spc, kTileRows)) = u[h][i];
+                    }
+                }
+                if constexpr (C::QTM)
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                else
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 vtc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_ready[t]);
@@ -677,22 +666,41 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             // that met a NaN: NaN (m = +infinity, which no other range outweighs)
             const bool zero = mask == 0 || (m_used == -INFINITY && l == 0.0f);
             const int64_t prow = ((int64_t)blockIdx.x * 2 + !w.at_start) * C::ROWS + t * kTileRows + r;
-            const float f = 1.0f / l;
+            const float f = zero ? 0.0f : w.whole ? 1.0f / l : 1.0f;
+            const int64_t drow = !rvalid ? -1 : w.whole ? orow : prow;  // the row's place
+            const bool half = w.whole && a.out_bf16;
+            uint8_t *base8 = static_cast<uint8_t *>(w.whole ? a.out : a.ws_o);
+            int64_t to[8];  // the rows that this lane writes a piece of
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(0xffffffffu, drow, i * 4 + srow);
+            // 128 bytes of every row at a time, all eight pieces under way together
+            auto put = [&](int part, int parts) {
+                __syncwarp();
+                uint4 u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = *at(i * 4 + srow, spc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (to[i] >= 0) *reinterpret_cast<uint4 *>(base8 + (to[i] * parts + part) * 128 + spc * 16) = u[i];
+                __syncwarp();
+            };
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 16) {
-                float v[16];
-                if (alive) {
-                    vtc::tmem_ld16(t_o + c0, v);
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                float v[32];
+                if (alive) vtc::tmem_ld_row<32>(t_o + c0, v);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = zero ? 0.0f : v[i] * f;
+                if (half) {
+                    const int j0 = (c0 / 32 & 1) * 4;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *at(lane, j0 + j) = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                                       pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+                    if (j0) put(c0 / 64, D / 64);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-                }
-                if (!rvalid) continue;
-                if (w.whole) {
-                    store_out16<D>(a, orow, c0, v, f, zero);
-                } else {
-                    store_ws8(a.ws_o + prow * D + c0, v);
-                    store_ws8(a.ws_o + prow * D + c0 + 8, v + 8);
+                    for (int j = 0; j < 8; ++j) *at(lane, j) = *reinterpret_cast<uint4 *>(v + 4 * j);
+                    put(c0 / 32, D / 32);
                 }
             }
             if (rvalid && !w.whole) {
