@@ -26,6 +26,11 @@
  * single launch mixing drafting and verifying requests (cross-resource
  * staggering, "Verifying Without Giving Back the Speedup", Figure 2).
  *
+ * A round may also draft a tree: vc_rotary_kv_write (rotary positions in
+ * general form, slots of their own), vc_tree_plan, vc_tree_attn (the tree's
+ * verification pass), vc_tree_accept, vc_tree_commit, and vc_token_logprobs
+ * (log probabilities, entropy and the alternatives a tree is drawn from).
+ *
  * Conventions
  *  - Every pointer argument named as "device" must point to device memory of
  *    the current device; "host" pointers to host memory.  The caller owns and
@@ -576,7 +581,7 @@ typedef struct {
  *  qkv         device, qkv_dtype VC_F32 or VC_BF16: row r at qkv + r *
  *              row_stride values, (Hq + 2 Hkv) heads of head_dim contiguous
  *              channels (Q heads, K heads, V heads).
- *              row_stride >= (Hq + 2 Hkv) head_dim.
+ *              row_stride >= (Hq + 2 Hkv) head_dim (at most 2^28).
  *  row_req     device int32 [m]: request; -1 = a padding row, nothing of
  *              which is read or written.
  *  row_pos     device int32 [m]: position that sets the angle (>= 0).
@@ -628,8 +633,10 @@ VC_API vc_status vc_tree_plan(const int32_t *parent, int32_t batch, int32_t n_q,
  *              or VC_BF16 (the probabilities enter the second product in bf16
  *              either way, as in vc_verify_attn)
  * Limits and the other arguments are vc_verify_attn's; softmax_scale > 0; the
- * pools, q and out lie on 16-byte boundaries, the workspace on a 32-byte one.  A request with seq_lens[b] < n_q, or of
- * more than max_seq_len, gets VC_ERR_BAD_INDEX in dev_status and zeros.
+ * pools, q and out lie on 16-byte boundaries, the workspace on a 32-byte one
+ * (calls that may run at the same time take one each).  A request with
+ * seq_lens[b] < n_q, or of more than max_seq_len or max_blocks pages, gets
+ * VC_ERR_BAD_INDEX in dev_status and zeros.
  * Entries of the tree that a node does not attend to do not touch its result,
  * whatever they hold (infinities and NaN included); a node that attends to an
  * entry of the tree whose V holds one gets NaN in all channels.  The context
@@ -656,7 +663,8 @@ VC_API vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, c
  *              order, -1 behind them
  *  emitted     device int32 [batch][n_q]: the a accepted tokens, then
  *              verified[path[a]]; -1 behind them
- * For a chain (parent[i] = i - 1) this is the rule of vc_accept.
+ * For a chain (parent[i] = i - 1) this is the rule of vc_accept.  The outputs
+ * overlap neither one another nor the inputs.
  */
 VC_API vc_status vc_tree_accept(const int32_t *parent, const int32_t *tokens, const int32_t *verified,
                                 int32_t batch, int32_t n_q, int32_t *accept_len, int32_t *path, int32_t *emitted,
@@ -672,6 +680,7 @@ VC_API vc_status vc_tree_accept(const int32_t *parent, const int32_t *tokens, co
  *            batch, max_blocks, num_pages, block_table and seq_lens (still
  *            the length with the tree); each has pools of its own, on
  *            16-byte boundaries (a pool given twice is refused).
+ * The pages that hold a request's tree are its own (not shared with another).
  * A path that does not ascend strictly from 0 and stay below n_q, a length
  * outside [-1, n_q - 1] or seq_lens[b] < n_q leave the request as it was, and
  * a bad page that entry (VC_ERR_BAD_INDEX in dev_status).
@@ -690,7 +699,7 @@ VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int
  *  ids           device int32 [rows][n_ids], n_ids >= 0: the tokens asked for.
  *                -1 is no token (log probability 0); any other id outside [0,
  *                vocab) gets 0 too and is reported (VC_ERR_BAD_INDEX)
- *  temperature   tau > 0
+ *  temperature   tau > 0 (and above 2^-127, where 1 / tau is still a float)
  *  logprobs      device fp32 [rows][n_ids]
  *  entropy       device fp32 [rows], or NULL
  *  top_ids       device int32 [rows][top_k], 0 <= top_k <= 64: the ids of the
@@ -698,7 +707,8 @@ VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int
  *                Logits of -infinity are not listed: -1 fills the rest
  *  top_logprobs  device fp32 [rows][top_k], -infinity beside a -1
  *  workspace     vc_token_logprobs_workspace_bytes(rows, vocab, top_k) bytes,
- *                8-byte aligned
+ *                8-byte aligned (calls that may run at the same time take one
+ *                each)
  * Logits of -infinity (tokens ruled out) have probability 0 and add nothing
  * to the entropy.  A row of nothing else gives -infinity (given tokens), 0
  * (entropy) and an empty list.  A row that holds NaN or +infinity has no
@@ -719,7 +729,8 @@ VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t ro
  * use).  Every wait of a kernel on a copy or on another warp gives up after
  * a time limit, reports VC_ERR_TIMEOUT in dev_status and lets the block
  * drain and exit (no GPU hang on a lost copy).  This sets that limit for the
- * draft, draft-step, verification and mixed launches made after the call:
+ * draft, draft-step, verification, mixed and tree launches made after the
+ * call:
  * wait_limit_ns in (0, 2e9], or 0 for the default of 2 s.  skip_copies != 0
  * makes those kernels issue none of their KV page copies (and signal none),
  * so every wait on a copy runs into the limit: outputs are then zeros and

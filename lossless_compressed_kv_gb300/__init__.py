@@ -504,6 +504,8 @@ def _cache(kv: PagedKV, dev: int) -> PagedKVStruct:
     n = k.shape[0]
     if v.shape[0] != n or not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("the page pools must be contiguous and of one size")
+    if kv.bits == 16 and not k.nbytes == v.nbytes == n * kv.num_kv_heads * kv.head_dim * 32:
+        raise ValueError("a page holds num_kv_heads x 16 rows of head_dim bf16 values")
     return PagedKVStruct(_here("k_pages", k, dev), _here("v_pages", v, dev), n,
                          _need("block_table", table, _I32, (b, w), dev), _need("seq_lens", lens, _I32, (b,), dev), b, w,
                          KVFormat(kv.num_kv_heads, kv.head_dim, kv.bits))
@@ -628,10 +630,12 @@ def token_logprobs(logits, ids, logprobs, workspace, temperature: float = 1.0, e
     rows, vocab = logits.shape
     if vocab > 1 and logits.stride(1) != 1:
         raise ValueError("the rows of logits must be contiguous")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs come together")
     dev = _device()
-    n_ids, k, ti, tl = ids.shape[1], 0, None, None
+    n_ids, k, ti, tl = ids.shape[-1], 0, None, None
     if top_ids is not None:
-        k = top_ids.shape[1]
+        k = top_ids.shape[-1]
         ti = _need("top_ids", top_ids, _I32, (rows, k), dev)
         tl = _need("top_logprobs", top_logprobs, _F32, (rows, k), dev)
     _check(_lib.vc_token_logprobs(

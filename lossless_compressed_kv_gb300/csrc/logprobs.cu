@@ -288,7 +288,8 @@ __device__ inline Stats join_stats(Stats a, Stats b, float inv_tau) {
 // too): r in units, t in units of log 2; those of packs that a thread holds.
 // y = scale (v - m) takes one multiply-add, scale v - h with h = scale m rounded:
 // every y is then too large by the same d = scale m - h, which is known and
-// comes off at the end (e^y by 2^-d, y e^y by d e^y as well).
+// comes off at the end (e^y by 2^-d, y e^y by d e^y as well).  t is NaN where
+// that cannot be done: -infinity among the logits, h or d out of range.
 template <typename T, int NV>
 __device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float scale, float &r, float &t) {
     using P = Pack<T>;
@@ -314,6 +315,8 @@ __device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float sc
     r = r2[0] + r2[1];
     t = f * __fmaf_rn(-d, r, t2[0] + t2[1]);
     r *= f;
+    // (from |h| = 2^30 on, d may reach sizes whose 2^d leaves fp32's range)
+    if (!(fabsf(d) < 64.0f)) t = __int_as_float(0x7fffffff);
 }
 // The same where -infinity may be among them (0 times infinity above; here a
 // bound keeps it out of y e^y: e^y is 0 long before) or the maximum, which is
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             float r = 0.0f, t = 0.0f;
             if (mine > -INFINITY && mine < INFINITY && wm < INFINITY) {
                 sums_of<T, NV>(x, held, mine, scale, r, t);
-                if (!(t <= 0.0f)) {  // -infinity is among them
+                if (!(t <= 0.0f)) {  // -infinity is among them, or h is out of range
                     int c = 0;
                     r = t = 0.0f;
 #pragma unroll
@@ -812,12 +815,13 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
     Stats s{-INFINITY, 0.0f, 0.0f, 0.0f};
     int n = 0;
     bool nan = false;
+    auto keys_of = [&](int p) { return (int)min(w[p * size + 2], (unsigned long long)a.k); };
     for (int p = 0; p < a.parts; ++p) {
         const float2 mc = *reinterpret_cast<const float2 *>(w + p * size);
         const float2 rt = *reinterpret_cast<const float2 *>(w + p * size + 1);
         nan = nan || mc.x != mc.x;
         s = join_stats(s, {mc.x, mc.y, rt.x, rt.y}, a.inv_tau);
-        n += (int)w[p * size + 2];
+        n += keys_of(p);
     }
     if (nan) s.m = __int_as_float(0x7fffffff);
     // a key's place is the number of larger ones: among all of them in shared
@@ -828,7 +832,7 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
     if (all <= kJoinKeys) {
         for (int i = threadIdx.x; i < all; i += blockDim.x) {
             const int p = i / a.k, j = i % a.k;
-            keys[i] = j < (int)w[p * size + 2] ? w[p * size + 3 + j] : 0;
+            keys[i] = j < keys_of(p) ? w[p * size + 3 + j] : 0;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < all; i += blockDim.x) {
@@ -841,12 +845,12 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
     } else {
         for (int i = threadIdx.x; i < all; i += blockDim.x) {
             const int p = i / a.k, j = i % a.k;
-            if (j >= (int)w[p * size + 2]) continue;
+            if (j >= keys_of(p)) continue;
             const unsigned long long key = w[p * size + 3 + j];
             int rank = j;
             for (int o = 0; o < a.parts; ++o) {
                 if (o == p) continue;
-                const int no = (int)w[o * size + 2];
+                const int no = keys_of(o);
                 for (int q = 0; q < no && w[o * size + 3 + q] > key; ++q) ++rank;
             }
             if (rank < a.k) top[rank] = key;
@@ -912,9 +916,12 @@ vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int
     if (rows < 0 || vocab < 1 || row_stride < vocab || n_ids < 0 || top_k < 0 || !(temperature > 0.0f) ||
         !std::isfinite(temperature))
         return VC_ERR_INVALID_ARG;
-    if (dtype_bytes(dtype) == 0 || top_k > VC_MAX_TOP || vocab > kVocabMax) return VC_ERR_UNSUPPORTED;
+    const int bytes = dtype_bytes(dtype);
+    const float inv_tau = 1.0f / temperature;
+    if (bytes == 0 || top_k > VC_MAX_TOP || vocab > kVocabMax || !std::isfinite(inv_tau * kLog2e))
+        return VC_ERR_UNSUPPORTED;
     if (rows == 0) return VC_OK;
-    if (!logits || (n_ids > 0 && (!ids || !logprobs)) || (top_k > 0 && (!top_ids || !top_logprobs)))
+    if (!logits || (uintptr_t)logits % bytes || (n_ids > 0 && (!ids || !logprobs)) || (top_k > 0 && (!top_ids || !top_logprobs)))
         return VC_ERR_INVALID_ARG;
     if ((uintptr_t)workspace & 7) return VC_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < vc_token_logprobs_workspace_bytes(rows, vocab, top_k))
@@ -928,7 +935,7 @@ vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int
     a.ids = ids;
     a.n_ids = n_ids;
     a.k = top_k;
-    a.inv_tau = 1.0f / temperature;
+    a.inv_tau = inv_tau;
     a.lp = logprobs;
     a.ent = entropy;
     a.top_ids = top_ids;

@@ -16,6 +16,7 @@ namespace vc {
 namespace {
 
 constexpr int kMaxPairs = VC_MAX_HEAD_DIM / 2;
+constexpr int kMaxWidth = 1 << 28;  // channels of a row of qkv
 
 struct RotArgs {
     const void *qkv;
@@ -242,10 +243,13 @@ extern "C" vc_status vc_rotary_kv_write(const void *qkv, int32_t qkv_dtype, int6
     if (!paged_fmt_ok(full) || m < 0 || num_q_heads < 1 || !rotary_ok(rotary, full->fmt.head_dim) ||
         row_stride < ((int64_t)num_q_heads + 2 * (int64_t)full->fmt.num_kv_heads) * full->fmt.head_dim)
         return VC_ERR_INVALID_ARG;
-    if (full->fmt.bits != 16 || (qkv_dtype != VC_F32 && qkv_dtype != VC_BF16)) return VC_ERR_UNSUPPORTED;
+    if (full->fmt.bits != 16 || (qkv_dtype != VC_F32 && qkv_dtype != VC_BF16) ||
+        ((int64_t)num_q_heads + 2 * (int64_t)full->fmt.num_kv_heads) * full->fmt.head_dim > kMaxWidth)
+        return VC_ERR_UNSUPPORTED;
     if (m == 0 || full->batch == 0) return VC_OK;
     if (!qkv || !row_req || !row_pos || !q_out || !full->k_pages || !full->v_pages || !full->block_table ||
-        full->max_blocks < 1 || full->num_pages < 1)
+        full->max_blocks < 1 || full->num_pages < 1 || (uintptr_t)qkv % dtype_bytes(qkv_dtype) ||
+        (((uintptr_t)q_out | (uintptr_t)full->k_pages | (uintptr_t)full->v_pages) & 1))
         return VC_ERR_INVALID_ARG;
     RotArgs a;
     a.qkv = qkv;

@@ -89,7 +89,13 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
                        void *workspace, size_t workspace_bytes, int32_t *dev_status, vc_stream_t stream) {
     if (!paged_fmt_ok(full) || max_seq_len < 0 || n_q < 1 || !(softmax_scale > 0.0f) || !std::isfinite(softmax_scale))
         return VC_ERR_INVALID_ARG;
-    if (!verify_supported(full->fmt, num_q_heads, n_q) || (out_dtype != VC_F32 && out_dtype != VC_BF16))
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!verify_supported(full->fmt, num_q_heads, n_q) || (out_dtype != VC_F32 && out_dtype != VC_BF16) ||
+        !std::isfinite(scale_log2))
+        return VC_ERR_UNSUPPORTED;
+    // (the kernel counts blocks in 32 bits)
+    const int64_t held = (int64_t)full->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
+    if ((longest / tree::Cfg<128, 1>::BK + 1) * full->batch * full->fmt.num_kv_heads > INT32_MAX)
         return VC_ERR_UNSUPPORTED;
     if (full->batch == 0) return VC_OK;
     if (!q || !mask || !out || !paged_ok(full) || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) ||
@@ -110,8 +116,8 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
     a.hq = num_q_heads;
     a.hkv = full->fmt.num_kv_heads;
     a.grp = num_q_heads / a.hkv;
-    a.max_len = max_seq_len;
-    a.scale_log2 = softmax_scale * 1.4426950408889634f;
+    a.max_len = (int)longest;
+    a.scale_log2 = scale_log2;
     a.ws_o = (float *)workspace;
     a.out = out;
     a.out_bf16 = out_dtype == VC_BF16;

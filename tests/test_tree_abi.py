@@ -152,3 +152,42 @@ def test_wrappers_refuse_tensors(vc):
     with pytest.raises(ValueError):
         vc.tree_attn(torch.zeros((2, 4, 1, 128), dtype=torch.bfloat16), kv, m, 1.0, torch.zeros((2, 4, 1, 128)), 16,
                      torch.zeros(8, dtype=torch.uint8))
+
+
+def test_refusals_at_the_ends_of_the_ranges(vc):
+    """Addresses off their type's boundary, blocks that 32 bits do not count,
+    scales and temperatures whose base-2 form is not finite."""
+    L, S = vc.library(), vc.STATUS
+    odd = C.c_void_p((1 << 20) + 1)
+    assert rotary_call(vc, rot(vc), cache(vc), qkv=odd) == "VC_ERR_INVALID_ARG"
+    assert rotary_call(vc, rot(vc), cache(vc), dtype=1, qkv=odd) == "VC_ERR_INVALID_ARG"
+    assert rotary_call(vc, rot(vc), cache(vc, k=(1 << 20) + 1)) == "VC_ERR_INVALID_ARG"
+    assert rotary_call(vc, rot(vc), cache(vc), hq=1 << 22, stride=1 << 40) == "VC_ERR_UNSUPPORTED"
+
+    def attn(scale, batch=1, blocks=1, longest=64):
+        c = cache(vc, batch=batch)
+        c.max_blocks = blocks
+        return S[L.vc_tree_attn(FAKE, 4, 4, C.byref(c), FAKE, scale, FAKE, 1, longest, FAKE, 0, None, None)]
+
+    assert attn(3e38) == "VC_ERR_UNSUPPORTED"
+    assert attn(1.0, 1 << 20, 1 << 20, 2 ** 31 - 1) == "VC_ERR_UNSUPPORTED"
+    assert attn(1.0, 1 << 20, 1 << 20, 64) == "VC_ERR_WORKSPACE"         # counted by what can be reached
+    assert attn(1.0, 1, 1, 2 ** 31 - 1) == "VC_ERR_WORKSPACE"
+
+    def lp(dtype, tau, logits=FAKE):
+        return S[L.vc_token_logprobs(logits, dtype, 1, 8, 8, None, 0, tau, 0, None, None, None, None, FAKE, 0, None,
+                                     None)]
+
+    assert lp(0, 1e-39) == "VC_ERR_UNSUPPORTED"
+    assert lp(0, 1.0) == "VC_ERR_WORKSPACE"
+    for dtype in (0, 1, 2):
+        assert lp(dtype, 1.0, odd) == "VC_ERR_INVALID_ARG"
+    assert lp(0, 1.0, C.c_void_p((1 << 20) + 2)) == "VC_ERR_INVALID_ARG"
+
+
+def test_wrappers_refuse_halves(vc):
+    x, i = torch.zeros((2, 8)), torch.zeros((2, 1), dtype=torch.int32)
+    with pytest.raises(ValueError, match="come together"):
+        vc.token_logprobs(x, i, x[:, :1], x, top_ids=i)
+    with pytest.raises(ValueError, match="come together"):
+        vc.token_logprobs(x, i, x[:, :1], x, top_logprobs=x[:, :1])
