@@ -32,20 +32,9 @@ struct Plan {
 };
 int plans_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len, Plan (&p)[2]) {
     const int tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows);
-    auto plan = [&](int t0, int t1) {
-        const bool one = t1 - t0 == 1;
-        const int lanes = t1 - t0 == 4 ? 2 : 1, most = (one ? 2 * tree::kSMs : tree::kSMs) / lanes;
-        const int bk = one ? tree::Cfg<128, 1>::BK : tree::Cfg<128, 2>::BK;
-        const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, bk);
-        return Plan{t0, t1, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most),
-                    (one ? 1 : 2) * tree::kTileRows};
-    };
-    if (tiles == 3) {
-        p[0] = plan(0, 2);
-        p[1] = plan(2, 3);
-        return 2;
-    }
-    p[0] = plan(0, tiles);
+    const int lanes = tiles == 4 ? 2 : 1, most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / lanes;
+    const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, tree::Cfg<128, 1>::BK);
+    p[0] = Plan{0, tiles, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most), (tiles == 4 ? 2 : tiles) * tree::kTileRows};
     return 1;
 }
 // (the launches of a call follow one another: they share the workspace)
@@ -134,9 +123,9 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
         a.lanes = p[i].lanes;
         a.groups = p[i].groups;
         a.ws_ml = a.ws_o + (size_t)p[i].slots() * d;
-        const bool one = p[i].rows == tree::kTileRows;
-        const cudaError_t e = d == 64 ? (one ? launch<64, 1>(a, st) : launch<64, 2>(a, st))
-                                      : (one ? launch<128, 1>(a, st) : launch<128, 2>(a, st));
+        const int qt = p[i].rows / tree::kTileRows;
+        const cudaError_t e = d == 64 ? (qt == 1 ? launch<64, 1>(a, st) : qt == 2 ? launch<64, 2>(a, st) : launch<64, 3>(a, st))
+                                      : (qt == 1 ? launch<128, 1>(a, st) : qt == 2 ? launch<128, 2>(a, st) : launch<128, 3>(a, st));
         if (e != cudaSuccess) return VC_ERR_CUDA;
     }
     return VC_OK;

@@ -75,7 +75,10 @@ struct Cfg {
     // to fetch its A operand from TMEM whatever N is, and the math of N = 128
     // takes 68: two-tile CTAs, which the tensor core bounds, take 128 keys and
     // keep Q in shared memory; one-tile CTAs, which memory bounds, take 64.
-    static constexpr int BK = QT == 1 ? 64 : 128;
+    static constexpr int BK = QT == 2 ? 128 : 64;
+    static constexpr int NBUF = QT == 1 ? 1 : QT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
+    static constexpr bool EACH = NBUF > QT;
+    static_assert(NBUF <= 2 * QT, "");
     static constexpr int PG = BK / kPage;    // pages of a block
     static constexpr int SLOT = BK * D * 2;  // one block of K or of V
     static constexpr bool QTM = QT == 1;     // Q in TMEM
@@ -89,12 +92,13 @@ struct Cfg {
     static_assert(SLOTS >= 5 && SLOTS / 2 + 2 <= kBadRing, "ring depth");
     static constexpr int OFF_STAGE = OFF_KV + SLOTS * SLOT;
     static constexpr int OFF_BAR = OFF_STAGE + STAGE;
-    static constexpr int NBAR = 4 * QT + 2 * SLOTS + 1;  // q, s, p, o per tile; full, empty; tail
+    static constexpr int NS = NBUF < QT ? QT : NBUF;
+    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 1;  // q, pv, o per tile; s; p per buffer; full, empty; tail
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 16;
     static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "shared memory of the CTAs an SM holds");
     // TMEM columns: S (then P) and O of each tile, Q (bf16 pairs)
-    static constexpr int O_COL0 = QT * BK;
+    static constexpr int O_COL0 = NBUF * BK;
     static constexpr int Q_COL0 = O_COL0 + QT * D;
     static constexpr int TMEM_USED = Q_COL0 + (QTM ? D / 2 : 0);
     static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
@@ -102,8 +106,8 @@ struct Cfg {
     static constexpr int SM_WARPS = QT * 4;  // softmax warps
     // two-tile CTAs: the third warpgroup (producer, MMA issue, two idle warps)
     // gives registers up for the softmax warps, which hold 128 scores each
-    static constexpr int WARPS = QT == 1 ? 6 : 12;
-    static constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;  // 2 x 128 x 216 + 128 x 72 = 384 x 168
+    static constexpr int WARPS = QT == 1 ? 6 : 4 * QT + 4;
+    static constexpr int REGS_SOFTMAX = QT == 2 ? 208 : 136, REGS_OTHER = QT == 2 ? 88 : 96;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int MIN_CTAS = QT == 1 ? 2 : 1;
     static constexpr int ROWS = QT * kTileRows;
@@ -300,8 +304,8 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     }
     uint8_t *sq = smem;
     uint64_t *q_ready = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [QT]
-    uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + QT, *o_done = p_ready + QT;
-    uint64_t *full = o_done + QT, *empty = full + C::SLOTS, *tail = empty + C::SLOTS;
+    uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + C::NS, *o_done = p_ready + C::NBUF, *pv_done = o_done + QT;
+    uint64_t *full = pv_done + QT, *empty = full + C::SLOTS, *tail = empty + C::SLOTS;
     unsigned long long *bad = reinterpret_cast<unsigned long long *>(smem + C::OFF_MISC);  // [kBadRing]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad + kBadRing);
 
@@ -315,10 +319,11 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     if (tid == 0) {
         for (int t = 0; t < QT; ++t) {
             mbar_init(&q_ready[t], 4);
-            mbar_init(&s_ready[t], 1);
-            mbar_init(&p_ready[t], 4);
             mbar_init(&o_done[t], 1);
+            mbar_init(&pv_done[t], 1);
         }
+        for (int i = 0; i < C::NS; ++i) mbar_init(&s_ready[i], 1);
+        for (int i = 0; i < C::NBUF; ++i) mbar_init(&p_ready[i], 4);
         for (int i = 0; i < C::SLOTS; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -350,7 +355,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
 
     if (warp == C::SM_WARPS) {
         // ================= producer =================
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+        if constexpr (QT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         if (!a.skip_copies) {
             uint32_t seq = 0;   // copies into the ring so far
             int seg = 0;
@@ -465,79 +470,98 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
         }
     } else if (warp == C::SM_WARPS + 1) {
         // ================= MMA issue (the warp in step, one elected thread) =================
-        if constexpr (QT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
-        uint32_t seq = 0;            // copies taken from the ring
-        uint32_t done = 0, seg = 0;  // blocks and segments
+        if constexpr (QT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
         // (a descriptor's address field counts 16 bytes: steps are added to it)
         const uint64_t qd0 = vtc::sdesc(smem_u32(sq), 16, 1024);
         const uint64_t kd0 = vtc::sdesc(smem_u32(skv), 16, 1024), vd0 = vtc::sdesc(smem_u32(skv), BK * 128, 1024);
-        auto issue_s = [&](int t, uint32_t slot) {
+        auto issue_s = [&](int t, uint32_t buf, uint32_t slot) {
             const uint64_t kd = kd0 + slot * (C::SLOT / 16), qd = qd0 + t * (C::QTILE / 16);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t ko = ((ks >> 2) * (BK * 128) + (ks & 3) * 32) / 16;
                 if constexpr (C::QTM)
-                    umma_ta(tmem + t * BK, tmem + C::Q_COL0 + ks * 8, kd + ko, IQK, ks > 0);
+                    umma_ta(tmem + buf * BK, tmem + C::Q_COL0 + ks * 8, kd + ko, IQK, ks > 0);
                 else
-                    umma(tmem + t * BK, qd + ((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) / 16, kd + ko, IQK, ks > 0);
+                    umma(tmem + buf * BK, qd + ((ks >> 2) * (kTileRows * 128) + (ks & 3) * 32) / 16, kd + ko, IQK, ks > 0);
             }
-            umma_commit(&s_ready[t]);
+            umma_commit(&s_ready[C::NBUF < QT ? t : buf]);
         };
-        auto issue_pv = [&](int t, uint32_t slot, bool add) {
+        auto issue_pv = [&](int t, uint32_t buf, uint32_t slot, bool add) {
             const uint64_t vd = vd0 + slot * (C::SLOT / 16);
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
-                umma_ta(tmem + C::O_COL0 + t * D, tmem + t * BK + kk * 8, vd + kk * 16 * 128 / 16, IPV, add || kk > 0);
+                umma_ta(tmem + C::O_COL0 + t * D, tmem + buf * BK + kk * 8, vd + kk * 16 * 128 / 16, IPV, add || kk > 0);
         };
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            alive = __all_sync(0xffffffffu, mbar_wait(bar, parity, a.status, a.wait_ns));
-            vtc::tc_fence_after();
-            return alive;
-        };
-        auto wait_copy = [&](uint32_t q) { return wait(&full[q % C::SLOTS], (q / C::SLOTS) & 1); };
-        while (alive && w.next(a)) {
-            const int n = w.seg_n;
-            if (!wait_copy(seq)) break;
-            for (int t = 0; t < nt && alive; ++t)
-                if (wait(&q_ready[t], seg & 1)) issue_s(t, seq % C::SLOTS);
-            if (!alive) break;
-            umma_commit(&empty[seq % C::SLOTS]);
-            ++seq;
-            for (int j = 0; j < n && alive; ++j) {
-                const bool more = j + 1 < n;
-                // both copies first: a wait or a commit between P V and S lets
-                // the tensor core run dry (256 rows at 131072 keys: 453 instead
-                // of 421 us)
-                if (!wait_copy(seq) || (more && !wait_copy(seq + 1))) break;
-                for (int t = 0; t < nt; ++t) {
-                    if (!wait(&p_ready[t], done & 1)) break;
-                    issue_pv(t, seq % C::SLOTS, j > 0);
-                    if (more)
-                        issue_s(t, (seq + 1) % C::SLOTS);
-                    else
-                        umma_commit(&o_done[t]);
-                }
-                if (!alive) break;
-                ++done;
-                umma_commit(&empty[seq % C::SLOTS]);
-                ++seq;
-                if (more) {
-                    umma_commit(&empty[seq % C::SLOTS]);
-                    ++seq;
+        // places in the ring (K and V of a block lie side by side, so each steps by
+        // two) and among the S buffers, with the parity of the phase waited for there
+        struct Place {
+            uint32_t i, par;
+            __device__ void step(uint32_t by, uint32_t of) {
+                if ((i += by) >= of) {
+                    i -= of;
+                    par ^= 1;
                 }
             }
-            ++seg;
+        } kp{0, 0}, vp{1, 0}, pp{0, 0};
+        uint32_t sb = 0, seg = 0;
+        auto wait1 = [&](uint64_t *bar, uint32_t par) {
+            alive = __all_sync(0xffffffffu, mbar_wait(bar, par, a.status, a.wait_ns));
+            return alive;
+        };
+        auto wait = [&](bool p, bool v, bool k, int q) {
+            if (p && !wait1(&p_ready[pp.i], pp.par)) return false;
+            if (v && !wait1(&full[vp.i], vp.par)) return false;
+            if (k && !wait1(&full[kp.i], kp.par)) return false;
+            if (q >= 0 && !wait1(&q_ready[q], seg & 1)) return false;
+            vtc::tc_fence_after();
+            return true;
+        };
+        // S of the next step, which is one of tile t
+        auto next_s = [&](int t) {
+            issue_s(t, sb, kp.i);
+            if (++sb == C::NBUF) sb = 0;
+            if (t == QT - 1) {
+                umma_commit(&empty[kp.i]);
+                kp.step(2, C::SLOTS);
+            }
+        };
+        for (;; ++seg) {
+            const bool any = alive && w.next(a);
+            const int n = __shfl_sync(0xffffffffu, any ? w.seg_n : 0, 0);
+            if (n == 0) break;
+#pragma unroll
+            for (int i = 0; i < C::NBUF; ++i) {
+                if (i / QT >= n) break;
+                if (!wait(false, false, i % QT == 0, i < QT ? i : -1)) break;
+                next_s(i % QT);
+            }
+            for (int j = 0; j < n && alive; ++j) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    const int t2 = (t + C::NBUF) % QT;  // tile of the step that is NBUF ahead
+                    const bool more = j + (t + C::NBUF) / QT < n;
+                    if (!wait(true, t == 0, more && t2 == 0, t + C::NBUF < QT && j == 0 ? t2 : -1)) break;
+                    issue_pv(t, pp.i, vp.i, j > 0);
+                    pp.step(1, C::NBUF);
+                    if (C::EACH) umma_commit(&pv_done[t]);
+                    if (more) next_s(t2);
+                    if (j + 1 == n) umma_commit(&o_done[t]);
+                }
+                if (!alive) break;
+                umma_commit(&empty[vp.i]);
+                vp.step(2, C::SLOTS);
+            }
         }
-    } else if (QT == 2 && warp >= C::SM_WARPS) {
+    } else if (QT > 1 && warp >= C::SM_WARPS) {
         // (idle warps of that warpgroup)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     } else if ((warp >> 2) < nt) {
         // ================= softmax: one thread per row =================
-        if constexpr (QT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
+        if constexpr (QT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
         const int t = warp >> 2;
         const int r = (warp & 3) * 32 + lane;  // row within the tile = TMEM lane
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lane_base + t * BK, t_o = tmem + lane_base + C::O_COL0 + t * D;
+        const uint32_t t_o = tmem + lane_base + C::O_COL0 + t * D;
         const int rg = (tile0 + t) * kTileRows + r;
         const bool rvalid = rg < a.n_q * a.grp;
         const int qi = rvalid ? rg / a.grp : 0, qn = rvalid ? rg % a.grp : 0;
@@ -596,7 +620,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             float m_used = -INFINITY, l = 0.0f;
             // tcgen05.ld / st are warp-collective: every lane runs them together
             for (int j = 0; j < w.seg_n && alive; ++j, ++it) {
-                alive = __all_sync(0xffffffffu, mbar_wait(&s_ready[t], it & 1, a.status, a.wait_ns));
+                const uint32_t step = it * nt + t, buf = step % C::NBUF, t_s = tmem + lane_base + buf * BK;
+                alive = __all_sync(0xffffffffu, mbar_wait(&s_ready[C::NBUF < QT ? t : buf], (C::NBUF < QT ? it : step / C::NBUF) & 1, a.status,
+                                                             a.wait_ns));
                 if (!alive) break;
                 vtc::tc_fence_after();
                 float s[BK];
@@ -618,6 +644,11 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 // (rare after the first block): then O is rescaled
                 const bool grow = mb > m_used + 8.0f;
                 if (__any_sync(0xffffffffu, grow) && j > 0) {
+                    if constexpr (C::EACH) {
+                        alive = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (it - 1) & 1, a.status, a.wait_ns));
+                        if (!alive) break;
+                        vtc::tc_fence_after();
+                    }
                     const float f = grow ? (m_used == -INFINITY ? 0.0f : ex2(m_used - mb)) : 1.0f;
 #pragma unroll 1
                     for (int c0 = 0; c0 < D; c0 += 16) {
@@ -649,7 +680,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 vtc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[t]);
+                if (lane == 0) mbar_arrive(&p_ready[buf]);
                 l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
             }
             if (alive)
