@@ -24,25 +24,18 @@ __global__ void __launch_bounds__(tree::kJoinWarps * 32)
     tree::tree_join_block<D, QT>(a, warps_per_row);
 }
 
-// How a launch is laid out over the GPU; a call takes one, or two for three
-// tiles of rows (see tree_tc.cuh).
+// How a call is laid out over the GPU (see tree_tc.cuh).
 struct Plan {
-    int tile0, tiles, lanes, groups, rows;  // rows: of a CTA
-    int64_t slots() const { return (int64_t)groups * lanes * 2 * rows; }  // partial rows in the workspace
+    int tiles, lanes, groups;  // tiles of a CTA, CTAs per group, groups
+    int64_t slots() const { return (int64_t)groups * lanes * 2 * tiles * tree::kTileRows; }  // partial rows
 };
-int plans_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len, Plan (&p)[2]) {
-    const int tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows);
-    const int lanes = tiles == 4 ? 2 : 1, most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / lanes;
+Plan plan_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len) {
+    const int tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows), lanes = tiles == 4 ? 2 : 1;
     const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, tree::Cfg<128, 1>::BK);
-    p[0] = Plan{0, tiles, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most), (tiles == 4 ? 2 : tiles) * tree::kTileRows};
-    return 1;
+    const int most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / lanes;
+    return {tiles / lanes, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most)};
 }
-// (the launches of a call follow one another: they share the workspace)
-size_t workspace_of(const Plan *p, int n, int d) {
-    int64_t most = 0;
-    for (int i = 0; i < n; ++i) most = p[i].slots() > most ? p[i].slots() : most;
-    return (size_t)most * (d + 2) * sizeof(float);
-}
+size_t workspace_of(const Plan &p, int d) { return (size_t)p.slots() * (d + 2) * sizeof(float); }
 
 template <int D, int QT>
 cudaError_t launch(const tree::Args &a, cudaStream_t st) {
@@ -51,10 +44,9 @@ cudaError_t launch(const tree::Args &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(tree_kernel<D, QT>, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
     if (e != cudaSuccess) return e;
-    const int rows = min(a.n_q * a.grp, a.tiles * tree::kTileRows) - a.tile0 * tree::kTileRows;
     // ranges that a unit spans, were the lengths alike: a warp reads eight at once
     const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
-    const dim3 grid(a.batch * a.hkv, ceil_div(rows, tree::kJoinWarps / W));
+    const dim3 grid(a.batch * a.hkv, ceil_div(a.rows, tree::kJoinWarps / W));
     e = launch_pdl(tree_join_kernel<D, QT>, grid, tree::kJoinWarps * 32, 0, st, a, W);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -69,8 +61,7 @@ extern "C" {
 size_t vc_tree_workspace_bytes(const vc_paged_kv *full, int32_t n_q, int32_t num_q_heads, int32_t max_seq_len) {
     if (!full || full->batch < 0 || max_seq_len < 0 || n_q < 1 || !verify_supported(full->fmt, num_q_heads, n_q))
         return 0;
-    Plan p[2];
-    return workspace_of(p, plans_of(*full, n_q, num_q_heads, max_seq_len, p), full->fmt.head_dim);
+    return workspace_of(plan_of(*full, n_q, num_q_heads, max_seq_len), full->fmt.head_dim);
 }
 
 vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_paged_kv *full,
@@ -90,9 +81,9 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
     if (!q || !mask || !out || !paged_ok(full) || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) ||
         ((uintptr_t)full->k_pages & 15) || ((uintptr_t)full->v_pages & 15) || ((uintptr_t)workspace & 31))
         return VC_ERR_INVALID_ARG;
-    Plan p[2];
-    const int n = plans_of(*full, n_q, num_q_heads, max_seq_len, p), d = full->fmt.head_dim;
-    if (!workspace || workspace_bytes < workspace_of(p, n, d)) return VC_ERR_WORKSPACE;
+    const Plan p = plan_of(*full, n_q, num_q_heads, max_seq_len);
+    const int d = full->fmt.head_dim;
+    if (!workspace || workspace_bytes < workspace_of(p, d)) return VC_ERR_WORKSPACE;
     tree::Args a;
     a.q = (const uint16_t *)q;
     a.n_pages = full->num_pages;
@@ -116,19 +107,17 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
     if (!encode_pool(&a.kmap, full->k_pages, full->num_pages, a.hkv, d) ||
         !encode_pool(&a.vmap, full->v_pages, full->num_pages, a.hkv, d))
         return VC_ERR_CUDA;
+    a.rows = n_q * a.grp;
+    a.lanes = p.lanes;
+    a.groups = p.groups;
+    a.ws_ml = a.ws_o + (size_t)p.slots() * d;
     const cudaStream_t st = (cudaStream_t)stream;
-    for (int i = 0; i < n; ++i) {
-        a.tile0 = p[i].tile0;
-        a.tiles = p[i].tiles;
-        a.lanes = p[i].lanes;
-        a.groups = p[i].groups;
-        a.ws_ml = a.ws_o + (size_t)p[i].slots() * d;
-        const int qt = p[i].rows / tree::kTileRows;
-        const cudaError_t e = d == 64 ? (qt == 1 ? launch<64, 1>(a, st) : qt == 2 ? launch<64, 2>(a, st) : launch<64, 3>(a, st))
-                                      : (qt == 1 ? launch<128, 1>(a, st) : qt == 2 ? launch<128, 2>(a, st) : launch<128, 3>(a, st));
-        if (e != cudaSuccess) return VC_ERR_CUDA;
-    }
-    return VC_OK;
+    cudaError_t e;
+    if (d == 64)
+        e = p.tiles == 1 ? launch<64, 1>(a, st) : p.tiles == 2 ? launch<64, 2>(a, st) : launch<64, 3>(a, st);
+    else
+        e = p.tiles == 1 ? launch<128, 1>(a, st) : p.tiles == 2 ? launch<128, 2>(a, st) : launch<128, 3>(a, st);
+    return e == cudaSuccess ? VC_OK : VC_ERR_CUDA;
 }
 
 }  // extern "C"

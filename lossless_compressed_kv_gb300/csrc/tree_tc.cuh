@@ -17,17 +17,28 @@
 //
 // Tiles.  Rows are cut into tiles of 128 (one MMA's M).  One tile: CTAs of
 // one tile, two to an SM, which overlap each other's S / softmax / P V chain.
-// Two: CTAs of two tiles, one to an SM, whose tiles take turns on the tensor
-// core.  Four tiles: groups of two CTAs, two tiles each, on the same range in
-// step, so the second CTA finds K and V in L2.  Three tiles: a launch of two
-// and one of one.
+// Two and three: CTAs of two and three tiles, one to an SM, whose tiles take
+// turns on the tensor core.  Four: groups of two CTAs, two tiles each, on the
+// same range in step, so the second CTA finds K and V in L2.  (Three tiles as
+// a launch of two and one of one read K and V twice: 320 rows at 131072 keys
+// 728 us instead of 613.)
 //
 // A CTA: a producer warp that fills a ring of K and V blocks by TMA (one
-// 16-row x 64-channel box per page and 128-byte column), one thread that
-// issues the tcgen05.mma of all tiles in the order  P V (j), S (j + 1)  tile
-// by tile, and four softmax warps per tile (a thread owns a row = TMEM lane).
-// P (bf16) overwrites the S it came from.  S (j + 1) is issued behind P V (j),
-// so a finished S also says that O is at rest and may be rescaled.
+// 16-row x 64-channel box per page and 128-byte column), a warp that issues
+// the tcgen05.mma of all tiles, and four softmax warps per tile (a thread owns
+// a row = TMEM lane).  Step i is block i / tiles, tile i % tiles.  Its S goes to
+// S buffer i % NBUF, its P (bf16) overwrites that S, and behind P V (i) the
+// issue warp sends S (i + NBUF) into the buffer: the tensor core runs them in
+// order, so the buffer is free by then.  With no more buffers than tiles a
+// finished S also says that O is at rest and may be rescaled; with more, the
+// softmax warps wait for the P V before (rare: only when the maximum grows).
+//
+// Barriers are waited for by parity, which tells only the current phase from
+// the one before.  So a barrier's waiter must know that the phase before the
+// one it waits for is over: S barriers go by buffer where NBUF >= tiles (the
+// waiter has seen S (i - tiles), which came after S (i - NBUF)), else by tile;
+// P V barriers by tile (S (i) was issued behind P V (i - NBUF), and NBUF <= 2
+// tiles), the end of a segment has one of its own.
 //
 // The tree's own entries.  In blocks that reach into the tree a row's bits
 // pick the scores that count.  A V row that some nodes do not see must not
@@ -55,8 +66,8 @@ struct Args {
     const int32_t *table, *lens;
     const unsigned long long *mask;  // [B][n_q]
     int batch, maxb, n_q, hq, hkv, grp, max_len;
-    int lanes;        // CTAs per group
-    int tile0, tiles; // 128-row tiles [tile0, tiles) of a unit in this launch
+    int rows;    // of a unit
+    int lanes;   // CTAs per group
     int groups;  // G
     float scale_log2;
     float *ws_o;   // [CTA][2][rows of a CTA][D]
@@ -71,14 +82,17 @@ struct Args {
 template <int D, int QT>
 struct Cfg {
     static constexpr int NC = D / 64;        // 128-byte columns of a row
-    // Keys per block.  One S instruction (M 128, N = BK, K 16) takes 64 cycles
-    // to fetch its A operand from TMEM whatever N is, and the math of N = 128
-    // takes 68: two-tile CTAs, which the tensor core bounds, take 128 keys and
-    // keep Q in shared memory; one-tile CTAs, which memory bounds, take 64.
+    // Keys per block, S buffers.  An instruction of S (M 128, N = BK, K 16) takes
+    // about 64 cycles for its A operand whatever N is, and the math of N = 128
+    // 68: 128 keys where TMEM holds a buffer of that for each tile (256 rows at
+    // 131072 keys, head_dim 128: 397 us; 64 keys with four buffers: 450).  A
+    // third buffer for two tiles takes 64-channel heads from 172 to 154 us (256
+    // rows at 8 x 32768 keys), four for three tiles from 274 to 213.  One-tile
+    // CTAs, which memory bounds, take 64 keys, so that two fit an SM.
     static constexpr int BK = QT == 2 ? 128 : 64;
-    static constexpr int NBUF = QT == 1 ? 1 : QT == 2 ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 2);
-    static constexpr bool EACH = NBUF > QT;
-    static_assert(NBUF <= 2 * QT, "");
+    static constexpr int NBUF = QT == 1 ? (D == 64 ? 2 : 1) : QT == 2 ? (D == 64 ? 3 : 2) : D == 64 ? 4 : 2;
+    static constexpr bool AHEAD = NBUF > QT;
+    static_assert(NBUF <= 2 * QT, "phases that a parity tells apart");
     static constexpr int PG = BK / kPage;    // pages of a block
     static constexpr int SLOT = BK * D * 2;  // one block of K or of V
     static constexpr bool QTM = QT == 1;     // Q in TMEM
@@ -92,8 +106,8 @@ struct Cfg {
     static_assert(SLOTS >= 5 && SLOTS / 2 + 2 <= kBadRing, "ring depth");
     static constexpr int OFF_STAGE = OFF_KV + SLOTS * SLOT;
     static constexpr int OFF_BAR = OFF_STAGE + STAGE;
-    static constexpr int NS = NBUF < QT ? QT : NBUF;
-    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 1;  // q, pv, o per tile; s; p per buffer; full, empty; tail
+    static constexpr int NS = NBUF < QT ? QT : NBUF;  // S barriers: by buffer, or by tile
+    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 1;  // q, o, pv per tile; s; p per buffer; full, empty; tail
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 16;
     static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "shared memory of the CTAs an SM holds");
@@ -104,10 +118,11 @@ struct Cfg {
     static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
     static_assert(TMEM_USED <= (QT == 1 ? 256 : 512), "TMEM columns");
     static constexpr int SM_WARPS = QT * 4;  // softmax warps
-    // two-tile CTAs: the third warpgroup (producer, MMA issue, two idle warps)
-    // gives registers up for the softmax warps, which hold 128 scores each
+    // CTAs of more than one tile: the last warpgroup (producer, MMA issue, two idle
+    // warps) gives registers up for the softmax warps, which hold BK scores each
+    // (2 x 128 x 216 + 128 x 72 = 384 x 168; 3 x 128 x 136 + 128 x 96 = 64512 <= 512 x 128)
     static constexpr int WARPS = QT == 1 ? 6 : 4 * QT + 4;
-    static constexpr int REGS_SOFTMAX = QT == 2 ? 208 : 136, REGS_OTHER = QT == 2 ? 88 : 96;
+    static constexpr int REGS_SOFTMAX = QT == 2 ? 216 : 136, REGS_OTHER = QT == 2 ? 72 : 96;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int MIN_CTAS = QT == 1 ? 2 : 1;
     static constexpr int ROWS = QT * kTileRows;
@@ -311,7 +326,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int grp_id = blockIdx.x / a.lanes, glane = blockIdx.x % a.lanes;
-    const int tile0 = a.tile0 + QT * glane, nt = min(QT, a.tiles - tile0);  // this CTA's tiles
+    const int tile0 = QT * glane;  // this CTA's tiles: QT from there
 
     uint8_t *skv = smem + C::OFF_KV;
 
@@ -543,7 +558,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                     if (!wait(true, t == 0, more && t2 == 0, t + C::NBUF < QT && j == 0 ? t2 : -1)) break;
                     issue_pv(t, pp.i, vp.i, j > 0);
                     pp.step(1, C::NBUF);
-                    if (C::EACH) umma_commit(&pv_done[t]);
+                    if (C::AHEAD) umma_commit(&pv_done[t]);
                     if (more) next_s(t2);
                     if (j + 1 == n) umma_commit(&o_done[t]);
                 }
@@ -555,7 +570,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     } else if (QT > 1 && warp >= C::SM_WARPS) {
         // (idle warps of that warpgroup)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
-    } else if ((warp >> 2) < nt) {
+    } else {
         // ================= softmax: one thread per row =================
         if constexpr (QT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));
         const int t = warp >> 2;
@@ -563,7 +578,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + lane_base + C::O_COL0 + t * D;
         const int rg = (tile0 + t) * kTileRows + r;
-        const bool rvalid = rg < a.n_q * a.grp;
+        const bool rvalid = rg < a.rows;
         const int qi = rvalid ? rg / a.grp : 0, qn = rvalid ? rg % a.grp : 0;
         // the warp's 32 rows x 8 pieces of 16 bytes, on their way between a
         // thread's own row and eight neighbouring lanes a row (whole lines of
@@ -620,7 +635,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             float m_used = -INFINITY, l = 0.0f;
             // tcgen05.ld / st are warp-collective: every lane runs them together
             for (int j = 0; j < w.seg_n && alive; ++j, ++it) {
-                const uint32_t step = it * nt + t, buf = step % C::NBUF, t_s = tmem + lane_base + buf * BK;
+                const uint32_t step = it * QT + t, buf = step % C::NBUF, t_s = tmem + lane_base + buf * BK;
                 alive = __all_sync(0xffffffffu, mbar_wait(&s_ready[C::NBUF < QT ? t : buf], (C::NBUF < QT ? it : step / C::NBUF) & 1, a.status,
                                                              a.wait_ns));
                 if (!alive) break;
@@ -644,7 +659,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 // (rare after the first block): then O is rescaled
                 const bool grow = mb > m_used + 8.0f;
                 if (__any_sync(0xffffffffu, grow) && j > 0) {
-                    if constexpr (C::EACH) {
+                    if constexpr (C::AHEAD) {
                         alive = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], (it - 1) & 1, a.status, a.wait_ns));
                         if (!alive) break;
                         vtc::tc_fence_after();
@@ -770,9 +785,9 @@ __device__ __forceinline__ void tree_join_block(const Args &a, int W) {
     // groups whose ranges hold the unit's first and last block
     const int g0 = nblk > 0 ? deal.group_of(u0) : 0, g1 = nblk > 0 ? deal.group_of(u0 + nblk - 1) : -1;
     if (nblk > 0 && g0 == g1) return;  // finished there
-    const int rr = blockIdx.y * (kJoinWarps / W) + warp / W, rg = a.tile0 * kTileRows + rr;
-    const bool row_ok = rg < min(a.n_q * a.grp, a.tiles * kTileRows);
-    const int cta = rr / C::ROWS, trow = rr % C::ROWS;
+    const int rg = blockIdx.y * (kJoinWarps / W) + warp / W;
+    const bool row_ok = rg < a.rows;
+    const int cta = rg / C::ROWS, trow = rg % C::ROWS;
     float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.0f;
