@@ -519,6 +519,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             }
         } kp{0, 0}, vp{1, 0}, pp{0, 0};
         uint32_t sb = 0, seg = 0;
+        // What a step needs before its P V and the S ahead of it: its P, its V, that
+        // S's K and Q.  All first: a wait between P V and S lets the tensor core run
+        // dry (256 rows at 131072 keys: 453 instead of 421 us).
         auto wait1 = [&](uint64_t *bar, uint32_t par) {
             alive = __all_sync(0xffffffffu, mbar_wait(bar, par, a.status, a.wait_ns));
             return alive;
@@ -541,6 +544,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             }
         };
         for (;; ++seg) {
+            // (by shuffle, so that the compiler knows it, and with it the loops' state,
+            // to be uniform: what the tensor core's instructions take is then not
+            // moved there one by one; 64-key blocks, 256 rows: 450 instead of 632 us)
             const bool any = alive && w.next(a);
             const int n = __shfl_sync(0xffffffffu, any ? w.seg_n : 0, 0);
             if (n == 0) break;
