@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -464,23 +465,32 @@ _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat1
 
 
 # These wrappers run once per layer and step: pointers go to ctypes as plain
-# integers, the current device and stream are read once a call.
+# integers, structs are packed whole (a quarter of the time that setting their
+# fields takes), the current device and stream are read once a call.
+_PAGED_KV = struct.Struct("PPqPPiiiii4x").pack   # PagedKVStruct
+_ROTARY = struct.Struct("fiififff").pack         # RotaryStruct
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+    """The current CUDA device; -2, which no tensor is on, where there is none."""
+    if torch.cuda.is_initialized():
+        return _get_device()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
 def _need(name: str, t, dtype, shape, dev: int):
     """The address of a contiguous tensor of this type and shape on device dev."""
     if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s" % (name, dtype, tuple(shape)))
-    return _here(name, t, dev)
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device" % name)
+    return t.data_ptr()
 
 
 def _here(name: str, t, dev: int):
-    if not t.is_cuda or t.get_device() != dev:
+    if t.get_device() != dev:
         raise ValueError("%s must be on the current CUDA device" % name)
     return t.data_ptr()
 
@@ -499,16 +509,17 @@ def _on(stream, dev: int):
 
 def _cache(kv: PagedKV, dev: int) -> PagedKVStruct:
     """The struct of a cache whose four tensors are contiguous on device dev."""
-    k, v, table, lens = kv.k_pages, kv.v_pages, kv.block_table, kv.seq_lens
-    b, w = table.shape
-    n = k.shape[0]
-    if v.shape[0] != n or not k.is_contiguous() or not v.is_contiguous():
+    k, v, table = kv.k_pages, kv.v_pages, kv.block_table
+    hkv, d, bits = kv.num_kv_heads, kv.head_dim, kv.bits
+    ks, (b, w) = k.shape, table.shape
+    n = ks[0]
+    if v.shape != ks or not k.is_contiguous() or not v.is_contiguous():
         raise ValueError("the page pools must be contiguous and of one size")
-    if kv.bits == 16 and not k.nbytes == v.nbytes == n * kv.num_kv_heads * kv.head_dim * 32:
+    if bits == 16 and not k.numel() * k.itemsize == v.numel() * v.itemsize == n * hkv * d * 32:
         raise ValueError("a page holds num_kv_heads x 16 rows of head_dim bf16 values")
-    return PagedKVStruct(_here("k_pages", k, dev), _here("v_pages", v, dev), n,
-                         _need("block_table", table, _I32, (b, w), dev), _need("seq_lens", lens, _I32, (b,), dev), b, w,
-                         KVFormat(kv.num_kv_heads, kv.head_dim, kv.bits))
+    return PagedKVStruct.from_buffer_copy(_PAGED_KV(
+        _here("k_pages", k, dev), _here("v_pages", v, dev), n, _need("block_table", table, _I32, (b, w), dev),
+        _need("seq_lens", kv.seq_lens, _I32, (b,), dev), b, w, hkv, d, bits))
 
 
 @dataclass(frozen=True)
@@ -527,8 +538,9 @@ class Rotary:
     amplitude: float = 1.0
 
     def struct(self) -> RotaryStruct:
-        return RotaryStruct(self.theta, self.rot_dim, int(self.interleaved), self.factor, self.original_len,
-                            self.low_turns, self.high_turns, self.amplitude)
+        return RotaryStruct.from_buffer_copy(_ROTARY(self.theta, self.rot_dim, self.interleaved, self.factor,
+                                                     self.original_len, self.low_turns, self.high_turns,
+                                                     self.amplitude))
 
 
 def rotary_kv_write(qkv, row_req, row_pos, num_q_heads: int, rotary: Rotary, q_out, full: PagedKV, row_slot=None,
