@@ -64,7 +64,8 @@ __device__ inline float load1(const float *p) { return *p; }
 __device__ inline float load1(const uint16_t *p) { return bf16_bits_to_f32(*p); }
 __device__ inline uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// One block per row, one thread per channel pair of a head.
+// Rows, or an output, off 16-byte boundaries: one block per row, one thread per
+// channel pair of a head.
 template <typename T>
 __global__ void __launch_bounds__(256) rotary_pairs_kernel(const __grid_constant__ RotArgs a) {
     pdl_begin();
@@ -103,11 +104,18 @@ __global__ void __launch_bounds__(256) rotary_pairs_kernel(const __grid_constant
     }
 }
 
-// Rows whose halves (or pairs) come in whole 16-byte pieces of the output: a
-// block takes a few rows; their angles' sines go to shared memory once for all
-// heads, then a thread takes 8 output channels (interleaved, or copied ones) or
-// two times 8 (both halves of 8 pairs) at a time, 16-byte stores.  Bound by
-// memory: each value is read once and written once.
+// Rows on 16-byte boundaries: a block takes a few rows; their angles' cosines
+// and sines go to shared memory once for all heads, then a thread takes 8
+// channels at a time with 16-byte loads and stores.  Bound by memory: each value
+// is read once and written once (16384 rows of 32 + 8 + 8 heads of 128, fp32:
+// 93 us, 0.95 of a copy's rate).  How the pairs lie:
+//   kHalves      the halves are whole pieces: both pieces of 8 pairs at once
+//   kNeighbours  a pair is in one piece
+//   kOdd         the halves are not whole pieces: the other channel of each pair
+//                by itself, from the lines that a neighbour thread loads (50
+//                rotated channels of 128: 116 us; pair by pair, as rows off
+//                16-byte boundaries are taken, 158)
+enum Pairing { kHalves, kNeighbours, kOdd };
 constexpr int kThreadsV = 256;
 
 template <typename T>
@@ -132,7 +140,7 @@ __device__ inline void store8(uint16_t *p, const float (&v)[8]) {
 }
 
 constexpr int kMaxRows = 16;
-template <typename T, bool INTER>
+template <typename T, Pairing PAIRING>
 __global__ void __launch_bounds__(kThreadsV) rotary_wide_kernel(const __grid_constant__ RotArgs a, int rows) {
     pdl_begin();
     extern __shared__ float2 cs[];  // [rows][half]
@@ -144,8 +152,9 @@ __global__ void __launch_bounds__(kThreadsV) rotary_wide_kernel(const __grid_con
         cs[e] = cos_sin(a.turns[i], a.pos[r0 + k], a.amp);
     }
     __syncthreads();
-    // items of a row: per head, `turned` pieces that rotate, then copied ones
-    const int turned = INTER ? a.half / 4 : a.half / 8, plain = (a.d - 2 * a.half) / 8, per = turned + plain;
+    // items of a row: per head, `turned` ones that rotate, then copied ones
+    const int turned = PAIRING == kHalves ? a.half / 8 : (a.half + 3) / 4;
+    const int per = PAIRING == kHalves ? a.d / 16 : a.d / 8;
     const int items = (a.hq + 2 * a.hkv) * per;
     for (int f = threadIdx.x; f < n * items; f += kThreadsV) {
         const int k = f / items, e = f % items;
@@ -159,27 +168,12 @@ __global__ void __launch_bounds__(kThreadsV) rotary_wide_kernel(const __grid_con
                                            : a.vp + kv + (int64_t)(h - a.hq - a.hkv) * kPage * a.d;
         const bool turn = h < a.hq + a.hkv;
         float u[8];
-        if (i >= turned) {
-            const int ch = 2 * a.half + (i - turned) * 8;
-            load8(x + ch, u);
-            store8(dst + ch, u);
-        } else if (INTER) {
-            load8(x + i * 8, u);
-            if (turn) {
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const float2 w = c[i * 4 + p];
-                    const float y0 = u[2 * p] * w.x - u[2 * p + 1] * w.y;
-                    u[2 * p + 1] = u[2 * p + 1] * w.x + u[2 * p] * w.y;
-                    u[2 * p] = y0;
-                }
-            }
-            store8(dst + i * 8, u);
-        } else {
+        if constexpr (PAIRING == kHalves) {
+            const int c0 = i < turned ? i * 8 : a.half + i * 8 + (i - turned) * 8, c1 = i < turned ? c0 + a.half : c0 + 8;
             float v[8];
-            load8(x + i * 8, u);
-            load8(x + a.half + i * 8, v);
-            if (turn) {
+            load8(x + c0, u);
+            load8(x + c1, v);
+            if (turn && i < turned) {
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
                     const float2 w = c[i * 8 + p];
@@ -188,18 +182,50 @@ __global__ void __launch_bounds__(kThreadsV) rotary_wide_kernel(const __grid_con
                     u[p] = y0;
                 }
             }
+            store8(dst + c0, u);
+            store8(dst + c1, v);
+        } else {
+            load8(x + i * 8, u);
+            if (turn && i < turned) {
+                if constexpr (PAIRING == kNeighbours) {
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        if (i * 4 + p >= a.half) break;
+                        const float2 w = c[i * 4 + p];
+                        const float y0 = u[2 * p] * w.x - u[2 * p + 1] * w.y;
+                        u[2 * p + 1] = u[2 * p + 1] * w.x + u[2 * p] * w.y;
+                        u[2 * p] = y0;
+                    }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 8; ++p) {
+                        const int ch = i * 8 + p;
+                        if (ch >= 2 * a.half) break;
+                        const bool low = ch < a.half;
+                        const float2 w = c[low ? ch : ch - a.half];
+                        const float o = load1(x + (low ? ch + a.half : ch - a.half));
+                        u[p] = u[p] * w.x + (low ? -o : o) * w.y;
+                    }
+                }
+            }
             store8(dst + i * 8, u);
-            store8(dst + a.half + i * 8, v);
         }
     }
 }
 
-template <typename T, bool INTER>
+template <typename T, Pairing PAIRING>
 cudaError_t launch_wide(const RotArgs &a, cudaStream_t st) {
-    // a row a block while there are few; else about four pieces a thread
-    const int items = (a.hq + 2 * a.hkv) * a.d / (INTER ? 8 : 16);
+    // a row a block while there are few; else about four items a thread
+    const int items = (a.hq + 2 * a.hkv) * a.d / (PAIRING == kHalves ? 16 : 8);
     const int rows = a.m <= 1024 ? 1 : max(1, min(kMaxRows, 4 * kThreadsV / items));
-    return launch_pdl(rotary_wide_kernel<T, INTER>, ceil_div(a.m, rows), kThreadsV, rows * a.half * 8, st, a, rows);
+    return launch_pdl(rotary_wide_kernel<T, PAIRING>, ceil_div(a.m, rows), kThreadsV, rows * a.half * 8, st, a, rows);
+}
+template <typename T>
+cudaError_t launch(const RotArgs &a, bool wide, cudaStream_t st) {
+    if (!wide) return launch_pdl(rotary_pairs_kernel<T>, a.m, 256, 0, st, a);
+    return a.inter           ? launch_wide<T, kNeighbours>(a, st)
+           : a.half % 8 == 0 ? launch_wide<T, kHalves>(a, st)
+                             : launch_wide<T, kOdd>(a, st);
 }
 
 // F_i of every pair, from 64-bit frequencies.
@@ -273,18 +299,10 @@ extern "C" vc_status vc_rotary_kv_write(const void *qkv, int32_t qkv_dtype, int6
     a.batch = full->batch;
     a.status = dev_status;
     fill_turns(*rotary, a.turns);
-    // 16-byte pieces: 8 channels of the output, of 8 pairs' halves or 4 pairs
     const bool f32 = qkv_dtype == VC_F32;
-    const bool wide = a.half % (a.inter ? 4 : 8) == 0 && row_stride % (f32 ? 4 : 8) == 0 &&
+    const bool wide = row_stride % (f32 ? 4 : 8) == 0 &&
                       (((uintptr_t)qkv | (uintptr_t)q_out | (uintptr_t)a.kp | (uintptr_t)a.vp) & 15) == 0;
     const cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e;
-    if (wide)
-        e = f32 ? (a.inter ? launch_wide<float, true>(a, st) : launch_wide<float, false>(a, st))
-                : (a.inter ? launch_wide<uint16_t, true>(a, st) : launch_wide<uint16_t, false>(a, st));
-    else if (f32)
-        e = launch_pdl(rotary_pairs_kernel<float>, m, 256, 0, st, a);
-    else
-        e = launch_pdl(rotary_pairs_kernel<uint16_t>, m, 256, 0, st, a);
+    const cudaError_t e = f32 ? launch<float>(a, wide, st) : launch<uint16_t>(a, wide, st);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? VC_OK : VC_ERR_CUDA;
 }
