@@ -203,9 +203,6 @@ __device__ inline float warp_sum2(float u, float v, int lane) {
     return s;
 }
 
-__device__ inline void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ inline void bar_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
 // Puts n keys in order, by one warp: each one's place is the number of larger ones.
 __device__ inline void order_keys(const unsigned long long *cand, int n, int k, unsigned long long *top, int lane) {
     for (int i = lane; i < n; i += 32) {
@@ -351,38 +348,45 @@ __device__ inline void careful_sums(uint4 u, float m, float scale, float &r, flo
 // Bound by instructions and memory alike: 64 KB take an SM's share of the
 // bandwidth 1.4 us, and the main warps' 7 instructions a logit about as long.
 // ---------------------------------------------------------------------------
-constexpr int kMainWarps = 16, kMain = kMainWarps * 32, kFinishers = 4;
-constexpr int kRingThreads = kMain + 32 * (kFinishers + 1);
-constexpr int kRingCands = 512;  // logits not below the bound (more: the part is read again)
+constexpr int kMainWarps = 16, kPacks = 8;  // warps, packs a thread holds
+constexpr int kRingCands = 512;             // logits not below the bound (more: the part is read again)
 
-struct Hand {  // from the main warps to a finisher
-    float m[kMainWarps], t[kMainWarps];
-    float r[kMainWarps], top[kMainWarps];  // r apart: of the threads whose maximum is the warp's
-    float tmax[kMain];
+template <int GW>
+struct Hand {  // from the main warps of a part to a finisher
+    float m[GW], t[GW];
+    float r[GW], top[GW];  // r apart: of the threads whose maximum is the warp's
+    float tmax[GW * 32];
 };
-template <int NV>
+template <int GW>
 struct Ring {
-    static constexpr int STAGE = kMain * NV * 16, STAGES = NV >= 8 ? 3 : 8;
+    static constexpr int N = GW * 32, GROUPS = kMainWarps / GW;
+    static constexpr int STAGE = N * kPacks * 16, STAGES = GW == 16 ? 3 : GW == 8 ? 5 : 8;
+    static constexpr int FIN = GW == 16 ? 4 : 8;  // finishing warps
+    static constexpr int THREADS = 32 * (kMainWarps + FIN + 1);
     static constexpr int OFF_HAND = STAGE * STAGES;
-    static constexpr int OFF_CAND = OFF_HAND + kFinishers * (int)sizeof(Hand);
-    static constexpr int OFF_TOP = OFF_CAND + kFinishers * kRingCands * 8;
-    static constexpr int OFF_GRP = OFF_TOP + kFinishers * VC_MAX_TOP * 8;
-    static constexpr int OFF_LIST = OFF_GRP + kFinishers * 32 * 4;
-    static constexpr int OFF_COUNT = OFF_LIST + kFinishers * kMain * 2;
-    static constexpr int OFF_META = OFF_COUNT + kFinishers * 8;
+    static constexpr int OFF_CAND = OFF_HAND + FIN * (int)sizeof(Hand<GW>);
+    static constexpr int OFF_TOP = OFF_CAND + FIN * kRingCands * 8;
+    static constexpr int OFF_GRP = OFF_TOP + FIN * VC_MAX_TOP * 8;
+    static constexpr int OFF_LIST = OFF_GRP + FIN * 32 * 4;
+    static constexpr int OFF_COUNT = OFF_LIST + FIN * N * 2;
+    static constexpr int OFF_META = OFF_COUNT + FIN * 8;
     static constexpr int OFF_BAR = OFF_META + 64;
     static_assert(STAGES * 4 <= 64, "packs of a stage");
-    static constexpr int SMEM = OFF_BAR + 2 * STAGES * 8;
+    // (the part FIN behind another is loaded after that one's stage, and with it
+    // its finisher's Hand, came free)
+    static_assert(STAGES <= FIN, "a Hand is written once it has been read");
+    static constexpr int SMEM = OFF_BAR + (2 * STAGES + FIN) * 8;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __grid_constant__ LpArgs a) {
+template <typename T, int GW>
+__global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(const __grid_constant__ LpArgs a) {
     pdl_wait();
     using P = Pack<T>;
-    using R = Ring<NV>;
-    constexpr int VEC = P::VEC;
+    using R = Ring<GW>;
+    constexpr int VEC = P::VEC, N = R::N, NV = kPacks;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR), *empty = full + R::STAGES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + R::OFF_BAR), *empty = full + R::STAGES, *ready = empty + R::STAGES;
     int *packs_of = reinterpret_cast<int *>(smem + R::OFF_META);  // of a stage
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t items = (int64_t)a.rows * a.parts;
@@ -393,6 +397,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
+        for (int i = 0; i < R::FIN; ++i) mbar_init(&ready[i], GW);
         fence_mbar_init();
     }
     __syncthreads();
@@ -414,15 +419,9 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
         q.packs = (q.n - q.head) / VEC;
         return q;
     };
-    int stage = 0, parity = 0;
-    auto step = [&]() {
-        if (++stage == R::STAGES) {
-            stage = 0;
-            parity ^= 1;
-        }
-    };
-    if (warp == kMainWarps + kFinishers) {
+    if (warp == kMainWarps + R::FIN) {
         // ---- producer ----
+        int stage = 0, parity = 0;
         int64_t sent = 0;
         for (int64_t item = blockIdx.x; item < items && alive; item += gridDim.x, ++sent) {
             const Part q = part_of(item);
@@ -438,7 +437,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                     mbar_arrive(&full[stage]);
                 }
             }
-            step();
+            if (++stage == R::STAGES) {
+                stage = 0;
+                parity ^= 1;
+            }
         }
         pdl_trigger();
         // no copy may be under way when the block ends
@@ -450,20 +452,20 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
     }
     if (warp < kMainWarps) {
         // ---- main warps ----
-        int f = 0;
-        int64_t k = 0;
-        for (int64_t item = blockIdx.x; item < items; item += gridDim.x, ++k) {
-            const uint8_t *src = smem + stage * R::STAGE + tid * 16;
-            alive = alive && mbar_wait(&full[stage], parity, a.status, kWaitNs);
+        const int gt = tid % N, gw = warp % GW;  // place in the group
+        for (uint32_t k = warp / GW; blockIdx.x + (int64_t)k * gridDim.x < items; k += R::GROUPS) {
+            const int stage = k % R::STAGES, f = k % R::FIN;
+            const uint8_t *src = smem + stage * R::STAGE + gt * 16;
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], k / R::STAGES & 1, a.status, kWaitNs))) break;
             // packs of this thread
-            const int packs = alive ? *(volatile int *)&packs_of[stage] : 0;
-            const int held = packs > tid ? min(NV, (packs - tid + kMain - 1) / kMain) : 0;
+            const int packs = *(volatile int *)&packs_of[stage];
+            const int held = packs > gt ? min(NV, (packs - gt + N - 1) / N) : 0;
             uint4 x[NV];
             float mine = -INFINITY;
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
                 if (j >= held) break;
-                x[j] = *reinterpret_cast<const uint4 *>(src + j * (kMain * 16));
+                x[j] = *reinterpret_cast<const uint4 *>(src + j * (N * 16));
                 mine = max_nan(mine, P::max_of(x[j]));
             }
             const float wm = warp_max_nan(mine);
@@ -491,42 +493,39 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 for (int o = 16; o > 0; o >>= 1) r_top += __shfl_xor_sync(0xffffffffu, r_top, o);
             }
             const float rt = warp_sum2(holds_top ? 0.0f : r, t, lane);
-            // (the finisher has read what it was handed before)
-            if (k >= kFinishers) bar_sync(1 + kFinishers + f, kMain + 32);
-            Hand &h = reinterpret_cast<Hand *>(smem + R::OFF_HAND)[f];
-            h.tmax[tid] = mine;
-            if (holds_top) h.top[warp] = r_top;
+            Hand<GW> &h = reinterpret_cast<Hand<GW> *>(smem + R::OFF_HAND)[f];
+            h.tmax[gt] = mine;
+            if (holds_top) h.top[gw] = r_top;
             if (lane == 0) {
-                h.m[warp] = wm;
-                h.r[warp] = rt;
+                h.m[gw] = wm;
+                h.r[gw] = rt;
             }
-            if (lane == 16) h.t[warp] = rt;
-            bar_arrive(1 + f, kMain + 32);
-            f = f + 1 == kFinishers ? 0 : f + 1;
-            step();
+            if (lane == 16) h.t[gw] = rt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[f]);
         }
         return;
     }
     // ---- finishing warps ----
     const int f = warp - kMainWarps;
-    const Hand &h = reinterpret_cast<const Hand *>(smem + R::OFF_HAND)[f];
+    const Hand<GW> &h = reinterpret_cast<const Hand<GW> *>(smem + R::OFF_HAND)[f];
     unsigned long long *cand = reinterpret_cast<unsigned long long *>(smem + R::OFF_CAND) + f * kRingCands;
     unsigned long long *top = reinterpret_cast<unsigned long long *>(smem + R::OFF_TOP) + f * VC_MAX_TOP;
     float *grp = reinterpret_cast<float *>(smem + R::OFF_GRP) + f * 32;
-    int16_t *list = reinterpret_cast<int16_t *>(smem + R::OFF_LIST) + f * kMain;
+    int16_t *list = reinterpret_cast<int16_t *>(smem + R::OFF_LIST) + f * N;
     int *count = reinterpret_cast<int *>(smem + R::OFF_COUNT) + f * 2;
-    stage = f % R::STAGES;
+    int stage = f % R::STAGES, parity = 0;
     int id_next = -1;
     if (a.parts == 1 && blockIdx.x + (int64_t)f * gridDim.x < items)
         id_next = asked_id(a, blockIdx.x + (int64_t)f * gridDim.x, lane);
-    for (int64_t item = blockIdx.x + (int64_t)f * gridDim.x; item < items; item += (int64_t)kFinishers * gridDim.x) {
+    for (int64_t item = blockIdx.x + (int64_t)f * gridDim.x; item < items; item += (int64_t)R::FIN * gridDim.x) {
         const Part q = part_of(item);
         const uint8_t *src = smem + stage * R::STAGE;
         const int id = id_next;
         typename P::Word logit = 0;
         if (a.parts == 1) {
             logit = asked_logit<T>(a, q.row, id);
-            const int64_t later = item + (int64_t)kFinishers * gridDim.x;
+            const int64_t later = item + (int64_t)R::FIN * gridDim.x;
             id_next = later < items ? asked_id(a, later, lane) : -1;
         }
         // a logit at an end of the part, beside the whole packs (at most 14)
@@ -534,24 +533,25 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
         typename P::Word loose_w = 0;
         const bool has_loose = loose_i >= 0 && loose_i < q.n;
         if (has_loose) loose_w = reinterpret_cast<const typename P::Word *>(q.p)[loose_i];
-        bar_sync(1 + f, kMain + 32);
+        if (!__all_sync(0xffffffffu, mbar_wait(&ready[f], parity, a.status, kWaitNs))) break;
+        parity ^= 1;
         const float loose = has_loose ? P::of(loose_w) : -INFINITY;
         Stats s;
-        const float wm = lane < kMainWarps ? h.m[lane] : -INFINITY;
+        const float wm = lane < GW ? h.m[lane] : -INFINITY;
         s.m = warp_max_nan(max_nan(wm, loose));
         s.c = s.r = s.t = 0.0f;
         const bool sound = s.m > -INFINITY && s.m < INFINITY;
         int have = 0, n = 0;
         float lo = s.m;
         if (sound) {
-            float tm[kMainWarps];  // maxima of the threads w * 32 + lane
+            float tm[GW];  // maxima of the threads w * 32 + lane
 #pragma unroll
-            for (int w = 0; w < kMainWarps; ++w) tm[w] = h.tmax[w * 32 + lane];
+            for (int w = 0; w < GW; ++w) tm[w] = h.tmax[w * 32 + lane];
             // the packs of `threads` listed threads, 32 at a time
             auto for_packs = [&](int threads, auto fn) {
                 for (int i0 = 0; i0 < threads * NV; i0 += 32) {
                     const int i = i0 + lane;
-                    int pk = i < threads * NV ? (i % NV) * kMain + list[i / NV] : -1;
+                    int pk = i < threads * NV ? (i % NV) * N + list[i / NV] : -1;
                     if (pk >= q.packs) pk = -1;
                     fn(pk);
                 }
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 t = fmaf(p, y, t);
             }
 #pragma unroll
-            for (int w = 0; w < kMainWarps; ++w) {
+            for (int w = 0; w < GW; ++w) {
                 const unsigned who = __ballot_sync(0xffffffffu, tm[w] == s.m);
                 if (!who) continue;
                 if (tm[w] == s.m) list[threads + __popc(who & ((1u << lane) - 1))] = (int16_t)(w * 32 + lane);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 // smallest maximum that fewer than k exceed
                 float g[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int w = 0; w < kMainWarps; ++w) g[w & 1] = fmaxf(g[w & 1], tm[w]);
+                for (int w = 0; w < GW; ++w) g[w & 1] = fmaxf(g[w & 1], tm[w]);
                 const bool two = a.k > 24;
                 if (!two) g[0] = fmaxf(g[0], g[1]);
                 int above[2] = {0, 0};
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 }
                 uint32_t mine = 0;
 #pragma unroll
-                for (int w = 0; w < kMainWarps; ++w) mine |= tm[w] >= floor ? 1u << w : 0u;
+                for (int w = 0; w < GW; ++w) mine |= tm[w] >= floor ? 1u << w : 0u;
                 if (mine)
                     for (int at = atomicAdd(&count[0], __popc(mine)); mine; mine &= mine - 1, ++at)
                         list[at] = (int16_t)((__ffs(mine) - 1) * 32 + lane);
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
                 for (int i0 = lane; i0 < packs; i0 += 128) {
                     auto pack_of = [&](int k) {
                         const int i = i0 + 32 * k;
-                        const int pk = i < packs ? (i % NV) * kMain + list[i / NV] : q.packs;
+                        const int pk = i < packs ? (i % NV) * N + list[i / NV] : q.packs;
                         return pk < q.packs ? pk : -1;
                     };
                     uint32_t in = 0;
@@ -662,8 +662,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) logprobs_ring_kernel(const __
         // stage and hand-over are free again
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
-        if (item + (int64_t)kFinishers * gridDim.x < items) bar_arrive(1 + kFinishers + f, kMain + 32);
-        stage = (stage + kFinishers) % R::STAGES;
+        stage = (stage + R::FIN) % R::STAGES;
         if (a.k > 0 && sound) {
             if (n <= kRingCands) {
                 order_keys(cand, n, a.k, top, lane);
@@ -865,19 +864,19 @@ __global__ void __launch_bounds__(128) logprobs_join_kernel(const __grid_constan
 // Parts of a row: packs of at most 64 KB, of one size, a multiple of 8 logits.
 constexpr int kVocabMax = 1 << 22;
 void split(int vocab, int dtype, int &parts, int &len) {
-    const int most = (kMain * 8 - 1) * (dtype == VC_F32 ? 4 : 8) / 8 * 8;  // (wherever it starts in its first pack)
+    const int most = (kMainWarps * 32 * kPacks - 1) * (dtype == VC_F32 ? 4 : 8) / 8 * 8;  // (wherever it starts in its first pack)
     parts = ceil_div(vocab, most);
     len = parts == 1 ? vocab : ceil_div(ceil_div(vocab, parts), 8) * 8;
     parts = ceil_div(vocab, len);
 }
 
-template <typename T, int NV>
+template <typename T, int GW>
 cudaError_t launch_ring(const LpArgs &a, cudaStream_t st) {
-    const cudaError_t e = set_smem_limit((const void *)logprobs_ring_kernel<T, NV>, Ring<NV>::SMEM);
+    const cudaError_t e = set_smem_limit((const void *)logprobs_ring_kernel<T, GW>, Ring<GW>::SMEM);
     if (e != cudaSuccess) return e;
     const int64_t items = (int64_t)a.rows * a.parts;
-    return launch_pdl(logprobs_ring_kernel<T, NV>, dim3((unsigned)(items < 152 ? items : 152)), kRingThreads,
-                      Ring<NV>::SMEM, st, a);
+    return launch_pdl(logprobs_ring_kernel<T, GW>, dim3((unsigned)(items < 152 ? items : 152)), Ring<GW>::THREADS,
+                      Ring<GW>::SMEM, st, a);
 }
 
 template <typename T>
@@ -890,7 +889,10 @@ cudaError_t launch(LpArgs a, int dtype, cudaStream_t st) {
         return launch_pdl(logprobs_short_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), kShortWarps * 32, 0,
                           st, a);
     }
-    cudaError_t e = packs <= kMain * 2 ? launch_ring<T, 2>(a, st) : launch_ring<T, 8>(a, st);
+    cudaError_t e = packs <= 2 * 32 * kPacks   ? launch_ring<T, 2>(a, st)
+                    : packs <= 4 * 32 * kPacks ? launch_ring<T, 4>(a, st)
+                    : packs <= 8 * 32 * kPacks ? launch_ring<T, 8>(a, st)
+                                               : launch_ring<T, 16>(a, st);
     if (e == cudaSuccess && a.parts > 1) e = launch_pdl(logprobs_join_kernel<T>, a.rows, 128, 0, st, a);
     return e;
 }
