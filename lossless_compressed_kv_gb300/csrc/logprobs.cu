@@ -581,9 +581,24 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
                 threads += __popc(who);
             }
             __syncwarp();
+            uint32_t first = loose == s.m ? q.v0 + loose_i : ~0u;  // id of a maximum: for k = 1 all that is asked
             for_packs(threads, [&](int pk) {
-                if (pk >= 0) careful_sums<T>(*reinterpret_cast<const uint4 *>(src + pk * 16), s.m, scale, r, unused, c);
+                if (pk < 0) return;
+                const uint4 u = *reinterpret_cast<const uint4 *>(src + pk * 16);
+                careful_sums<T>(u, s.m, scale, r, unused, c);
+                if (a.k == 1) {
+                    float v[VEC];
+                    P::unpack(u, v);
+#pragma unroll
+                    for (int e = VEC - 1; e >= 0; --e)
+                        if (v[e] == s.m) first = min(first, (uint32_t)(q.v0 + q.head + pk * VEC + e));
+                }
             });
+            if (a.k == 1) {
+                first = __reduce_min_sync(0xffffffffu, first);
+                if (lane == 0) top[0] = order_key(s.m, first);
+                have = 1;
+            }
             const float both = warp_sum2(r, t, lane);
             s.r = __shfl_sync(0xffffffffu, both, 0);
             s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
@@ -612,7 +627,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
                 if (two && above[1] < a.k) least = fminf(least, g[1]);
                 lo = -warp_max_nan(-least);
             }
-            if (a.k > 0) {
+            if (a.k > 1) {
                 // the logits not below it (and not -infinity), from the threads whose
                 // maximum is not, in an order left to chance (what follows is not)
                 const float floor = fmaxf(lo, -3.402823466e38f);
@@ -663,7 +678,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[stage]);
         stage = (stage + R::FIN) % R::STAGES;
-        if (a.k > 0 && sound) {
+        if (a.k > 1 && sound) {
             if (n <= kRingCands) {
                 order_keys(cand, n, a.k, top, lane);
                 have = min(a.k, n);
