@@ -338,15 +338,21 @@ __device__ inline void careful_sums(uint4 u, float m, float scale, float &r, flo
 // of 16 bytes each; the few logits at a part's ends that share a pack with
 // something else are the finisher's (padded with -infinity they would send two
 // main warps through the careful sums in every row: 4096 rows of 32001 bf16
-// logits 97 instead of 55 us).  16 main warps go through a part once: a thread takes NV packs of 16 bytes, their
-// maximum, and the sums relative to that; the warp's sums relative to the warp's
-// maximum.  They never meet.  One of 4 finishing warps, in turn, joins the
-// warps' sums, goes again through the 1/16 that holds the maximum to count it
-// apart, takes the k-th largest of 32 or 64 groups' maxima as a bound (k logits
-// at least are not below it), collects the logits not below it from the
-// threads whose maximum is not, puts them in order and writes the results.
-// Bound by instructions and memory alike: 64 KB take an SM's share of the
-// bandwidth 1.4 us, and the main warps' 7 instructions a logit about as long.
+// logits 97 instead of 55 us).  16 main warps, in groups of GW that take a part
+// each, go through it once: a thread takes up to 8 packs, their maximum, and the
+// sums relative to that; the warp's sums relative to the warp's maximum.  They
+// never meet.  A finishing warp joins the group's sums, goes again through the
+// threads' packs that hold the maximum to count it apart, takes the k-th largest
+// of 32 or 64 groups' maxima as a bound (k logits at least are not below it),
+// collects the logits not below it from the threads whose maximum is not, puts
+// them in order and writes the results, while the others work on later parts.
+// GW is the least whose threads hold a part (8, 16, 32 or 64 KB of it): with 16
+// warps to every part their fixed cost bounds (16384 bf16 rows of 4000 logits 89
+// instead of 55 us, of 15000 150 instead of 104).
+// Bound by memory for no or one alternative (16384 x 32000 bf16: 162 and 167 us,
+// 0.95 and 0.93 of a copy's rate; 8192 x 32000 fp32 157 us, 0.98); beyond by how
+// long a finisher holds its stage (20 alternatives: 243 us): three stages of 64 KB
+// fit.
 // ---------------------------------------------------------------------------
 constexpr int kMainWarps = 16, kPacks = 8;  // warps, packs a thread holds
 constexpr int kRingCands = 512;             // logits not below the bound (more: the part is read again)
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
             s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
             s.c = (float)__reduce_add_sync(0xffffffffu, c);
             if (a.k > 1) {
-                // 32 groups of 16 threads, for a larger k 64 of 8 (two a lane): the
+                // 32 groups of threads, for a larger k 64 (two a lane): the
                 // smallest maximum that fewer than k exceed
                 float g[2] = {-INFINITY, -INFINITY};
 #pragma unroll
