@@ -632,8 +632,6 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
                 float least = above[0] < a.k ? g[0] : INFINITY;
                 if (two && above[1] < a.k) least = fminf(least, g[1]);
                 lo = -warp_max_nan(-least);
-            }
-            if (a.k > 1) {
                 // the logits not below it (and not -infinity), from the threads whose
                 // maximum is not, in an order left to chance (what follows is not)
                 const float floor = fmaxf(lo, -3.402823466e38f);
