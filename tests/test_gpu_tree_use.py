@@ -181,3 +181,68 @@ def test_calls_of_logprobs_at_once(v):
     torch.cuda.synchronize()
     for o in jobs[:4]:
         assert all(torch.equal(a, b) for a, b in zip(o[:4], j[:4]))
+
+
+TILES = [(16, 16, 2), (32, 16, 2), (40, 16, 2), (64, 16, 2)]      # n_q, hq, hkv: 1 to 4 tiles of 128 rows
+
+
+@pytest.mark.parametrize("n_q,hq,hkv", TILES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_maxima_that_grow_block_by_block(n_q, hq, hkv, d):
+    """Keys that get longer for 16 blocks of 64, then start again: within a range
+    of a dozen blocks the running maximum rises by more than 2^8 most times, and
+    what is summed so far is scaled down each time."""
+    rng = np.random.default_rng([n_q, d])
+    lens = [int(x) for x in rng.integers(7000, 9000, 16)]
+    full, hf = H.full_cache(rng, lens, hkv, d)
+    kp = full.k_pages.view(torch.bfloat16).view(-1, hkv, 16, d)
+    for b, L in enumerate(lens):
+        pages = torch.as_tensor(hf["table"][b, :(L + 15) // 16].astype(np.int64), device="cuda")
+        f = 1 + 3 * ((torch.arange(len(pages), device="cuda") // 4) % 16)
+        kp[pages] = (kp[pages].float() * f.view(-1, 1, 1, 1)).to(torch.bfloat16)
+    hf["k"] = full.k_pages.cpu().numpy().view(hf["k"].dtype).reshape(hf["k"].shape)
+    qn, q = q_bf16(rng, (len(lens), n_q, hq, d))
+    masks = [T.tree_plan(random_parents(rng, n_q), L)[0] for L in lens]
+    scale = float(np.float32(d ** -0.5))
+    out, st = attn(full, q, to_mask(masks), scale, max(lens), torch.float32)
+    assert st == 0
+    for b in (0, 7, 15):
+        check_attn(out, hf, qn, masks[b], scale, b)
+
+
+@pytest.mark.parametrize("n_q,hq,hkv", TILES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("junk", [float("nan"), -float("inf")])
+def test_absent_nodes_may_hold_anything(n_q, hq, hkv, d, junk):
+    """Absent nodes and slots behind the request, whatever the tiles: the same bits."""
+    rng = np.random.default_rng([n_q, d, 1])
+    lens = [n_q, 700, 6000, 64 * 33, 128 * 21 + 1]
+    full, hf = H.full_cache(rng, lens, hkv, d)
+    qn, q = q_bf16(rng, (len(lens), n_q, hq, d))
+    parents = [random_parents(rng, n_q, absent=3) for _ in lens]
+    masks = [T.tree_plan(p, L)[0] for p, L in zip(parents, lens)]
+    clean, _ = attn(full, q, to_mask(masks), 0.1, max(lens))
+    for pool in (full.k_pages, full.v_pages):
+        p = pool.view(torch.bfloat16).view(-1, hkv, 16, d)
+        for b, L in enumerate(lens):
+            for pos in range(L - 3, (L + 15) // 16 * 16):
+                p[int(hf["table"][b, pos // 16]), :, pos % 16] = junk
+    out, st = attn(full, q, to_mask(masks), 0.1, max(lens))
+    assert st == 0 and torch.equal(out, clean) and bool((out[:, -3:] == 0).all())
+    for b in (0, 2):
+        check_attn(clean, hf, qn, masks[b], 0.1, b)
+
+
+def test_a_node_that_sees_an_infinite_value():
+    """... ends as NaN, and no other does, in any tile."""
+    n_q, hq, hkv, d, lens = 40, 8, 1, 128, [3000, 40]
+    full, hf, qn, q, _ = tree_case(3, lens, n_q, hq, hkv, d)
+    masks = [T.tree_plan([-1] + [i // 2 for i in range(n_q - 1)], L)[0] for L in lens]
+    clean, _ = attn(full, q, to_mask(masks), 0.1, max(lens))
+    vp = full.v_pages.view(torch.bfloat16).view(-1, hkv, 16, d)
+    pos = lens[0] - n_q + 5
+    vp[int(hf["table"][0, pos // 16]), :, pos % 16, 3] = float("inf")
+    out, st = attn(full, q, to_mask(masks), 0.1, max(lens))
+    sees = torch.tensor([bool(m >> 5 & 1) for m in masks[0]], device="cuda")
+    assert st == 0 and torch.equal(out[1], clean[1]) and 1 < int(sees.sum()) < n_q
+    assert out[0][sees].isnan().all() and torch.equal(out[0][~sees], clean[0][~sees])
