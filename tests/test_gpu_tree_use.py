@@ -246,3 +246,33 @@ def test_a_node_that_sees_an_infinite_value():
     sees = torch.tensor([bool(m >> 5 & 1) for m in masks[0]], device="cuda")
     assert st == 0 and torch.equal(out[1], clean[1]) and 1 < int(sees.sum()) < n_q
     assert out[0][sees].isnan().all() and torch.equal(out[0][~sees], clean[0][~sees])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("v,k", [(900, 3), (2100, 1), (2603, 30), (6001, 5), (8008, 0), (12001, 2), (20000, 1), (32000, 20),
+                                 (40001, 7)])
+def test_many_rows(dtype, v, k):
+    """Every row of a batch that keeps each block busy for a dozen of them: all
+    lengths of rows, all of whose results are checked (tolerances of
+    test_gpu_logprobs; the entropy's is 640 2^-24 (2 + 2 entropy))."""
+    m, rows, e = vc(), 2003, 2.0 ** -24
+    g = torch.Generator(device="cuda")
+    g.manual_seed(v)
+    x = (torch.randn((rows, v), generator=g, device="cuda") * 3).to(dtype)
+    ids = torch.randint(0, v, (rows, 2), generator=g, device="cuda", dtype=torch.int32)
+    lp, ent = torch.empty((rows, 2), device="cuda"), torch.empty(rows, device="cuda")
+    top, tlp = torch.empty((rows, k), dtype=torch.int32, device="cuda"), torch.empty((rows, k), device="cuda")
+    ws = torch.full((m.token_logprobs_workspace_bytes(rows, v, k),), 0xFF, dtype=torch.uint8, device="cuda")
+    m.token_logprobs(x, ids, lp, ws, entropy=ent, top_ids=top if k else None, top_logprobs=tlp if k else None)
+    torch.cuda.synchronize()
+    for r0 in range(0, rows, 500):
+        want = x[r0:r0 + 500].double().log_softmax(1)
+        w = want.gather(1, ids[r0:r0 + 500].long())
+        assert bool(((lp[r0:r0 + 500] - w).abs() <= 640 * e + 4 * e * w.abs()).all())
+        h = -(want.exp() * want).sum(1)
+        assert bool(((ent[r0:r0 + 500] - h).abs() <= 640 * e * (2 + 2 * h)).all())
+        if k:
+            order = x[r0:r0 + 500].float().sort(dim=1, descending=True, stable=True)[1][:, :k]    # equal logits by id
+            assert torch.equal(top[r0:r0 + 500].long(), order)
+            w = want.gather(1, order)
+            assert bool(((tlp[r0:r0 + 500] - w).abs() <= 640 * e + 4 * e * w.abs()).all())
