@@ -355,7 +355,6 @@ __device__ inline void careful_sums(uint4 u, float m, float scale, float &r, flo
 // fit.
 // ---------------------------------------------------------------------------
 constexpr int kMainWarps = 16, kPacks = 8;  // warps, packs a thread holds
-constexpr int kRingCands = 512;             // logits not below the bound (more: the part is read again)
 
 template <int GW>
 struct Hand {  // from the main warps of a part to a finisher
@@ -366,12 +365,13 @@ struct Hand {  // from the main warps of a part to a finisher
 template <int GW>
 struct Ring {
     static constexpr int N = GW * 32, GROUPS = kMainWarps / GW;
-    static constexpr int STAGE = N * kPacks * 16, STAGES = GW == 16 ? 3 : GW == 8 ? 5 : 8;
-    static constexpr int FIN = GW == 16 ? 4 : 8;  // finishing warps
+    static constexpr int STAGE = N * kPacks * 16, STAGES = GW == 16 ? 3 : GW == 8 ? 6 : 8;
+    static constexpr int FIN = GW == 16 ? 4 : GW == 8 ? 7 : 8;  // finishing warps
+    static constexpr int CANDS = GW == 8 ? 320 : 512;  // logits not below the bound (more: the part is read again)
     static constexpr int THREADS = 32 * (kMainWarps + FIN + 1);
     static constexpr int OFF_HAND = STAGE * STAGES;
     static constexpr int OFF_CAND = OFF_HAND + FIN * (int)sizeof(Hand<GW>);
-    static constexpr int OFF_TOP = OFF_CAND + FIN * kRingCands * 8;
+    static constexpr int OFF_TOP = OFF_CAND + FIN * CANDS * 8;
     static constexpr int OFF_GRP = OFF_TOP + FIN * VC_MAX_TOP * 8;
     static constexpr int OFF_LIST = OFF_GRP + FIN * 32 * 4;
     static constexpr int OFF_COUNT = OFF_LIST + FIN * N * 2;
@@ -381,6 +381,9 @@ struct Ring {
     // (the part FIN behind another is loaded after that one's stage, and with it
     // its finisher's Hand, came free)
     static_assert(STAGES <= FIN, "a Hand is written once it has been read");
+    // (copies land in any order, and a parity tells two phases apart: who waits for
+    // a phase must have seen the one before)
+    static_assert(STAGES % GROUPS == 0, "a stage's parts go to one group");
     static constexpr int SMEM = OFF_BAR + (2 * STAGES + FIN) * 8;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
     // ---- finishing warps ----
     const int f = warp - kMainWarps;
     const Hand<GW> &h = reinterpret_cast<const Hand<GW> *>(smem + R::OFF_HAND)[f];
-    unsigned long long *cand = reinterpret_cast<unsigned long long *>(smem + R::OFF_CAND) + f * kRingCands;
+    unsigned long long *cand = reinterpret_cast<unsigned long long *>(smem + R::OFF_CAND) + f * R::CANDS;
     unsigned long long *top = reinterpret_cast<unsigned long long *>(smem + R::OFF_TOP) + f * VC_MAX_TOP;
     float *grp = reinterpret_cast<float *>(smem + R::OFF_GRP) + f * 32;
     int16_t *list = reinterpret_cast<int16_t *>(smem + R::OFF_LIST) + f * N;
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
                         for (int e = 0; e < VEC; ++e) in |= v[e] >= floor ? 1u << (8 * k + e) : 0u;
                     }
                     if (in)
-                        for (int at = atomicAdd(&count[1], __popc(in)); in && at < kRingCands; in &= in - 1, ++at) {
+                        for (int at = atomicAdd(&count[1], __popc(in)); in && at < R::CANDS; in &= in - 1, ++at) {
                             const int bit = __ffs(in) - 1, pk = pack_of(bit / 8), e = bit % 8;
                             cand[at] = order_key(P::one(reinterpret_cast<const T *>(src + pk * 16) + e),
                                                  q.v0 + q.head + pk * VEC + e);
@@ -683,11 +686,11 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         if (lane == 0) mbar_arrive(&empty[stage]);
         stage = (stage + R::FIN) % R::STAGES;
         if (a.k > 1 && sound) {
-            if (n <= kRingCands) {
+            if (n <= R::CANDS) {
                 order_keys(cand, n, a.k, top, lane);
                 have = min(a.k, n);
             } else {
-                have = order_again<T>(q.p, q.v0, q.n, a.k, lo, cand, kRingCands, top, lane);
+                have = order_again<T>(q.p, q.v0, q.n, a.k, lo, cand, R::CANDS, top, lane);
             }
         }
         if (a.parts == 1) {
