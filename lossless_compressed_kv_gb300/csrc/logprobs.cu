@@ -286,9 +286,10 @@ __device__ inline Stats join_stats(Stats a, Stats b, float inv_tau) {
 // y = scale (v - m) takes one multiply-add, scale v - h with h = scale m rounded:
 // every y is then too large by the same d = scale m - h, which is known and
 // comes off at the end (e^y by 2^-d, y e^y by d e^y as well).  t is NaN where
-// that cannot be done: -infinity among the logits, h or d out of range.
+// that cannot be done: -infinity among the logits, h or d out of range.  Packs
+// in `skip` are left out.
 template <typename T, int NV>
-__device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float scale, float &r, float &t) {
+__device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float scale, float &r, float &t, uint32_t skip = 0) {
     using P = Pack<T>;
     constexpr int VEC = P::VEC;
     float r2[2] = {0.0f, 0.0f}, t2[2] = {0.0f, 0.0f};
@@ -296,6 +297,7 @@ __device__ inline void sums_of(const uint4 (&x)[NV], int held, float m, float sc
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         if (j >= held) break;
+        if (skip >> j & 1) continue;
         float v[VEC];
         P::unpack(x[j], v);
 #pragma unroll
@@ -348,7 +350,7 @@ __device__ inline void careful_sums(uint4 u, float m, float scale, float &r, flo
 // them in order and writes the results, while the others work on later parts.
 // GW is the least whose threads hold a part (8, 16, 32 or 64 KB of it): with 16
 // warps to every part their fixed cost bounds (16384 bf16 rows of 4000 logits 89
-// instead of 55 us, of 15000 150 instead of 104).
+// instead of 55 us, of 15000 150 instead of 95).
 // Bound by memory for no or one alternative (16384 x 32000 bf16: 162 and 167 us,
 // 0.95 and 0.93 of a copy's rate; 8192 x 32000 fp32 157 us, 0.98); beyond by how
 // long a finisher holds its stage (20 alternatives: 243 us): three stages of 64 KB
@@ -713,7 +715,9 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
 // ---------------------------------------------------------------------------
 constexpr int kShortWarps = 4, kShortPacks = 8, kShortCands = 256;
 
-template <typename T>
+// TOP: no alternative, one, or more (registers for each by itself: 16384 rows of
+// 1000 bf16 logits, top 5, 33 us in one kernel for all)
+template <typename T, int TOP>
 __global__ void __launch_bounds__(kShortWarps * 32, 8) logprobs_short_kernel(const __grid_constant__ LpArgs a) {
     pdl_begin();
     using P = Pack<T>;
@@ -732,6 +736,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8) logprobs_short_kernel(con
         const int held = packs > lane ? min(NV, (packs - lane + 31) / 32) : 0;
         uint4 x[NV];
         float mine = -INFINITY;
+        uint32_t apart = 0;  // packs that hold the maximum or an end of the row
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int i0 = (j * 32 + lane) * VEC - skew;
@@ -740,6 +745,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8) logprobs_short_kernel(con
             } else {  // an end of the row, or behind it
                 uint32_t w[4] = {P::kNone, P::kNone, P::kNone, P::kNone};
                 if (j < held) {
+                    apart |= 1u << j;
 #pragma unroll
                     for (int e = 0; e < VEC; ++e)
                         if (i0 + e >= 0 && i0 + e < n) {
@@ -766,31 +772,58 @@ __global__ void __launch_bounds__(kShortWarps * 32, 8) logprobs_short_kernel(con
         const bool sound = s.m > -INFINITY && s.m < INFINITY;
         int have = 0;
         if (sound) {
-            float r = 0.0f, t = 0.0f;
+            // the maximum counted apart, -infinity (behind an end, or of tokens ruled
+            // out) kept out of y e^y: such packs one by one, the others together (a
+            // thread's packs all one by one if one is: 16384 rows of 1000 bf16
+            // logits, top 5, 41 instead of 31 us)
+            float r = 0.0f, t = 0.0f, r1 = 0.0f, t1 = 0.0f;
             int c = 0;
-            if (mine < s.m) sums_of<T, NV>(x, held, s.m, scale, r, t);
-            if (mine == s.m || !(t <= 0.0f)) {
-                r = t = 0.0f;
+            if (mine == s.m) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
-                    if (j < held) careful_sums<T>(x[j], s.m, scale, r, t, c);
+                    if (P::max_of(x[j]) == s.m) apart |= 1u << j;
             }
+            sums_of<T, NV>(x, held, s.m, scale, r, t, apart);
+            if (!(t <= 0.0f)) {
+                r = t = 0.0f;
+                apart = ~0u;
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j < held && (apart >> j & 1)) careful_sums<T>(x[j], s.m, scale, r1, t1, c);
+            r += r1;
+            t += t1;
             __syncwarp();
             const float both = warp_sum2(r, t, lane);
             s.r = __shfl_sync(0xffffffffu, both, 0);
             s.t = __shfl_sync(0xffffffffu, both, 16) * 0.6931471805599453f;
             s.c = (float)__reduce_add_sync(0xffffffffu, c);
-            if (a.k > 0) {
-                // the k-th largest of the lanes' maxima is a bound
-                float lo = s.m;
-                if (a.k > 1) {
-                    int rank = 0;
-                    for (int q = 0; q < 32; ++q) {
-                        const float o = __shfl_sync(0xffffffffu, mine, q);
-                        rank += o > mine || (o == mine && q < lane);
+            if constexpr (TOP == 1) {  // the first that equals the maximum
+                uint32_t first = ~0u;
+                if (mine == s.m) {
+#pragma unroll
+                    for (int j = NV - 1; j >= 0; --j) {
+                        if (P::max_of(x[j]) != s.m) continue;
+                        float v[VEC];
+                        P::unpack(x[j], v);
+#pragma unroll
+                        for (int e = VEC - 1; e >= 0; --e)
+                            if (v[e] == s.m) first = (uint32_t)((j * 32 + lane) * VEC - skew + e);
                     }
-                    const unsigned hit = __ballot_sync(0xffffffffu, rank == a.k - 1);
-                    lo = hit ? __shfl_sync(0xffffffffu, mine, __ffs(hit) - 1) : -INFINITY;
+                }
+                first = __reduce_min_sync(0xffffffffu, first);
+                if (lane == 0) top[0] = order_key(s.m, first);
+                __syncwarp();
+                have = 1;
+            } else if constexpr (TOP > 1) {
+                // the k-th largest of the lanes' maxima is a bound
+                float lo;
+                float left = mine;
+                for (int above = 0;;) {  // (a lane at least drops out each time)
+                    lo = warp_max_nan(left);
+                    above += __popc(__ballot_sync(0xffffffffu, left == lo));
+                    if (above >= a.k || lo == -INFINITY) break;
+                    if (left == lo) left = -INFINITY;
                 }
                 if (lane == 0) counts[warp] = 0;
                 __syncwarp();
@@ -922,8 +955,10 @@ cudaError_t launch(LpArgs a, int dtype, cudaStream_t st) {
     const int packs = ceil_div(a.part_len + VEC - 1, VEC);  // wherever the row starts
     if (packs <= 32 * kShortPacks) {
         const int64_t blocks = ((int64_t)a.rows + kShortWarps - 1) / kShortWarps, most = 152 * 8;
-        return launch_pdl(logprobs_short_kernel<T>, dim3((unsigned)(blocks < most ? blocks : most)), kShortWarps * 32, 0,
-                          st, a);
+        const dim3 grid((unsigned)(blocks < most ? blocks : most));
+        return a.k == 0   ? launch_pdl(logprobs_short_kernel<T, 0>, grid, kShortWarps * 32, 0, st, a)
+               : a.k == 1 ? launch_pdl(logprobs_short_kernel<T, 1>, grid, kShortWarps * 32, 0, st, a)
+                          : launch_pdl(logprobs_short_kernel<T, 2>, grid, kShortWarps * 32, 0, st, a);
     }
     cudaError_t e = packs <= 2 * 32 * kPacks   ? launch_ring<T, 2>(a, st)
                     : packs <= 4 * 32 * kPacks ? launch_ring<T, 4>(a, st)
