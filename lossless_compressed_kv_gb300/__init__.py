@@ -606,15 +606,38 @@ def tree_accept(parent, tokens, verified, accept_len, path, emitted, stream=None
 
 class KVLayers:
     """The caches of a model's layers as vc_tree_commit takes them (they share
-    block table, lengths and format); built once, kept by the caller."""
+    block table, lengths and format); built once, kept by the caller.  Every
+    tree_commit sees the tensors that the caches carry then: one that was
+    rebound (shortened lengths, a grown table) or moved in place is read anew.
+    Of the caches' other fields those of the last reading count."""
 
     def __init__(self, caches):
-        self.caches = list(caches)
-        self.device = _device()
-        self.structs = (PagedKVStruct * len(self.caches))(*[_cache(c, self.device) for c in self.caches])
+        self.caches = tuple(caches)
+        self._read(_device())
 
     def __len__(self):
         return len(self.caches)
+
+    def _read(self, dev):
+        structs = (PagedKVStruct * len(self.caches))(*[_cache(c, dev) for c in self.caches])
+        # the tensors that the addresses were taken from: held until the next
+        # reading, so that no other tensor can come to lie where one of them was
+        self._held = [(c, k, v, t, n, k.data_ptr(), v.data_ptr()) for c, k, v, t, n in
+                      [(c, c.k_pages, c.v_pages, c.block_table, c.seq_lens) for c in self.caches]]
+        small = {id(t): t for h in self._held for t in h[3:5]}
+        self._small = [(t, t.data_ptr(), t.shape) for t in small.values()]
+        self.device, self.batch, self.structs = dev, structs[0].batch if len(structs) else 0, structs
+
+    def _as_read(self) -> bool:
+        """Whether the caches carry the tensors of the last reading, where they were."""
+        for c, k, v, t, n, kp, vp in self._held:
+            if (c.k_pages is not k or c.v_pages is not v or c.block_table is not t or c.seq_lens is not n
+                    or k.data_ptr() != kp or v.data_ptr() != vp):
+                return False
+        for t, p, shape in self._small:
+            if t.data_ptr() != p or t.shape != shape:
+                return False
+        return True
 
 
 def tree_commit(layers: KVLayers, accept_len, path, status=None, stream=None):
@@ -622,8 +645,10 @@ def tree_commit(layers: KVLayers, accept_len, path, status=None, stream=None):
     have put them, in every layer."""
     dev, shape = _device(), path.shape
     b, n_q = shape
-    if len(layers) and (layers.caches[0].batch != b or layers.device != dev):
-        raise ValueError("path must be [batch][n_q] of the caches, which must be on the current CUDA device")
+    if layers.device != dev or not layers._as_read():
+        layers._read(dev)
+    if len(layers) and layers.batch != b:
+        raise ValueError("path must be [batch][n_q] of the caches")
     _check(_lib.vc_tree_commit(
         layers.structs, len(layers), n_q, _need("accept_len", accept_len, _I32, (b,), dev),
         _need("path", path, _I32, shape, dev), _status(status, dev), _on(stream, dev)), "vc_tree_commit")
