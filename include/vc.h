@@ -712,9 +712,11 @@ VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int
  * Logits of -infinity (tokens ruled out) have probability 0 and add nothing
  * to the entropy.  A row of nothing else gives -infinity (given tokens), 0
  * (entropy) and an empty list.  A row that holds NaN or +infinity has no
- * distribution: NaN everywhere, -1 for every alternative.  Sums are fp32; S is
- * kept as the maxima's count plus the rest, so a row that is all but certain
- * keeps its digits.
+ * distribution: NaN everywhere, -1 for every alternative.  A row whose logits
+ * did not arrive within the time limit of the kernel's waits is given the same
+ * way, with VC_ERR_TIMEOUT in dev_status.  Sums are fp32; S is kept as the
+ * maxima's count plus the rest, so a row that is all but certain keeps its
+ * digits.
  */
 VC_API size_t vc_token_logprobs_workspace_bytes(int32_t rows, int32_t vocab, int32_t top_k);
 VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int32_t vocab,
@@ -729,13 +731,15 @@ VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t ro
  * use).  Every wait of a kernel on a copy or on another warp gives up after
  * a time limit, reports VC_ERR_TIMEOUT in dev_status and lets the block
  * drain and exit (no GPU hang on a lost copy).  This sets that limit for the
- * draft, draft-step, verification, mixed and tree launches made after the
- * call:
+ * draft, draft-step, verification, mixed, tree-attention and (rows of more
+ * than about 4 KB) token-log-probability launches made after the call:
  * wait_limit_ns in (0, 2e9], or 0 for the default of 2 s.  skip_copies != 0
- * makes those kernels issue none of their KV page copies (and signal none),
- * so every wait on a copy runs into the limit: outputs are then zeros and
- * nothing of the cache is read.  Calls racing with launches on other threads
- * see either setting.  VC_ERR_INVALID_ARG for a limit out of range.
+ * makes those kernels issue none of their copies (and signal none), so every
+ * wait on a copy runs into the limit: attention outputs are then zeros and
+ * nothing of the cache is read; log probabilities are as vc_token_logprobs
+ * says.  skip_copies == 2: of a token-log-probability launch only the blocks
+ * of odd index do so.  Calls racing with launches on other threads see either
+ * setting.  VC_ERR_INVALID_ARG for a limit out of range.
  */
 VC_API vc_status vc_debug_set_wait_fault(int64_t wait_limit_ns, int32_t skip_copies);
 

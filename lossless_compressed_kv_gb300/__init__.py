@@ -197,9 +197,9 @@ def comp_block_encode(codes, scales, zeros, head_dim: int, bits: int, kind: str)
     return blk
 
 
-def debug_set_wait_fault(wait_limit_ns: int = 0, skip_copies: bool = False):
+def debug_set_wait_fault(wait_limit_ns: int = 0, skip_copies: int = 0):
     """vc_debug_set_wait_fault (tests of the bounded device waits only)."""
-    _check(_lib.vc_debug_set_wait_fault(int(wait_limit_ns), int(bool(skip_copies))), "vc_debug_set_wait_fault")
+    _check(_lib.vc_debug_set_wait_fault(int(wait_limit_ns), int(skip_copies)), "vc_debug_set_wait_fault")
 
 
 def head_block_bytes(head_dim: int, bits: int) -> int:

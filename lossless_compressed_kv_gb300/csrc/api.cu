@@ -227,7 +227,7 @@ vc_status vc_mixed_attn(const int32_t *role, const void *q_draft, const vc_paged
 vc_status vc_debug_set_wait_fault(int64_t wait_limit_ns, int32_t skip_copies) {
     if (wait_limit_ns < 0 || wait_limit_ns > (int64_t)kWaitNs) return VC_ERR_INVALID_ARG;
     g_wait_fault.wait_ns = wait_limit_ns == 0 ? kWaitNs : (uint64_t)wait_limit_ns;
-    g_wait_fault.skip_copies = skip_copies != 0;
+    g_wait_fault.skip_copies = skip_copies == 2 ? 2 : skip_copies != 0;
     return VC_OK;
 }
 

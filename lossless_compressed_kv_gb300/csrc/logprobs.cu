@@ -141,6 +141,8 @@ struct LpArgs {
     int32_t *top_ids;
     float *top_lp;
     int32_t *status;
+    uint64_t wait_ns;
+    int skip_copies;
 };
 
 // What a row's logits amount to: the maximum, how many logits equal it, the
@@ -434,10 +436,11 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         // ---- producer ----
         int stage = 0, parity = 0;
         int64_t sent = 0;
-        for (int64_t item = blockIdx.x; item < items && alive; item += gridDim.x, ++sent) {
+        for (int64_t item = block_skips(a.skip_copies) ? items : blockIdx.x; item < items && alive;
+             item += gridDim.x, ++sent) {
             const Part q = part_of(item);
             if (sent >= R::STAGES)
-                alive = __all_sync(0xffffffffu, mbar_wait(&empty[stage], parity ^ 1, a.status, kWaitNs));
+                alive = __all_sync(0xffffffffu, mbar_wait(&empty[stage], parity ^ 1, a.status, a.wait_ns));
             if (!alive) break;
             if (lane == 0) {
                 *(volatile int *)&packs_of[stage] = q.packs;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
             }
         }
         pdl_trigger();
-        // no copy may be under way when the block ends
+        // no copy may be under way when the block ends (however short the waits' limit)
         for (int i = 0; i < R::STAGES && i < sent; ++i) {
             const int64_t uses = (sent - 1 - i) / R::STAGES;  // copies into slot i before its last one
             if (!mbar_wait(&full[i], uses & 1, a.status, kWaitNs)) break;
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         for (uint32_t k = warp / GW; blockIdx.x + (int64_t)k * gridDim.x < items; k += R::GROUPS) {
             const int stage = k % R::STAGES, f = k % R::FIN;
             const uint8_t *src = smem + stage * R::STAGE + gt * 16;
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], k / R::STAGES & 1, a.status, kWaitNs))) break;
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], k / R::STAGES & 1, a.status, a.wait_ns))) break;
             // packs of this thread
             const int packs = *(volatile int *)&packs_of[stage];
             const int held = packs > gt ? min(NV, (packs - gt + N - 1) / N) : 0;
@@ -544,12 +547,14 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         typename P::Word loose_w = 0;
         const bool has_loose = loose_i >= 0 && loose_i < q.n;
         if (has_loose) loose_w = reinterpret_cast<const typename P::Word *>(q.p)[loose_i];
-        if (!__all_sync(0xffffffffu, mbar_wait(&ready[f], parity, a.status, kWaitNs))) break;
+        // once a wait has run out, this part and the warp's later ones end as if a
+        // NaN were among their logits: no row keeps what its outputs held before
+        alive = alive && __all_sync(0xffffffffu, mbar_wait(&ready[f], parity, a.status, a.wait_ns));
         parity ^= 1;
         const float loose = has_loose ? P::of(loose_w) : -INFINITY;
         Stats s;
         const float wm = lane < GW ? h.m[lane] : -INFINITY;
-        s.m = warp_max_nan(max_nan(wm, loose));
+        s.m = alive ? warp_max_nan(max_nan(wm, loose)) : __int_as_float(0x7fffffff);
         s.c = s.r = s.t = 0.0f;
         const bool sound = s.m > -INFINITY && s.m < INFINITY;
         int have = 0, n = 0;
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(Ring<GW>::THREADS, 1) logprobs_ring_kernel(con
         }
         // stage and hand-over are free again
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0 && alive) mbar_arrive(&empty[stage]);
         stage = (stage + R::FIN) % R::STAGES;
         if (a.k > 1 && sound) {
             if (n <= R::CANDS) {
@@ -1014,6 +1019,8 @@ vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t rows, int
     a.top_ids = top_ids;
     a.top_lp = top_logprobs;
     a.status = dev_status;
+    a.wait_ns = wait_fault().wait_ns;
+    a.skip_copies = wait_fault().skip_copies;
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e = dtype == VC_F32    ? launch<float>(a, dtype, st)
                           : dtype == VC_BF16 ? launch<__nv_bfloat16>(a, dtype, st)

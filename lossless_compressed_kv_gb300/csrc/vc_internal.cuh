@@ -115,9 +115,10 @@ __device__ inline bool mbar_wait(uint64_t *bar, uint32_t parity, int32_t *st, ui
 // verification kernels skip their KV copies, read by every launch.
 struct WaitFault {
     uint64_t wait_ns = kWaitNs;
-    int skip_copies = 0;
+    int skip_copies = 0;  // 1: every block, 2: where the kernel tells them apart, blocks of odd index
 };
 WaitFault wait_fault();
+__device__ inline bool block_skips(int skip_copies) { return skip_copies == 1 || (skip_copies == 2 && (blockIdx.x & 1)); }
 
 // One bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned).
 __device__ inline void bulk_g2s(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
