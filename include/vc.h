@@ -636,7 +636,8 @@ VC_API vc_status vc_tree_plan(const int32_t *parent, int32_t batch, int32_t n_q,
  * pools, q and out lie on 16-byte boundaries, the workspace on a 32-byte one
  * (calls that may run at the same time take one each).  A request with
  * seq_lens[b] < n_q, or of more than max_seq_len or max_blocks pages, gets
- * VC_ERR_BAD_INDEX in dev_status and zeros.
+ * VC_ERR_BAD_INDEX in dev_status and zeros; a row whose keys did not all
+ * arrive within the time limit of the kernel's waits VC_ERR_TIMEOUT and zeros.
  * Entries of the tree that a node does not attend to do not touch its result,
  * whatever they hold (infinities and NaN included); a node that attends to an
  * entry of the tree whose V holds one gets NaN in all channels.  The context
@@ -737,9 +738,10 @@ VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t ro
  * makes those kernels issue none of their copies (and signal none), so every
  * wait on a copy runs into the limit: attention outputs are then zeros and
  * nothing of the cache is read; log probabilities are as vc_token_logprobs
- * says.  skip_copies == 2: of a token-log-probability launch only the blocks
- * of odd index do so.  Calls racing with launches on other threads see either
- * setting.  VC_ERR_INVALID_ARG for a limit out of range.
+ * says.  skip_copies == 2: of a tree-attention or token-log-probability
+ * launch only the blocks of odd index do so.  Calls racing with launches on
+ * other threads see either setting.  VC_ERR_INVALID_ARG for a limit out of
+ * range.
  */
 VC_API vc_status vc_debug_set_wait_fault(int64_t wait_limit_ns, int32_t skip_copies);
 

@@ -371,7 +371,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     if (warp == C::SM_WARPS) {
         // ================= producer =================
         if constexpr (QT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
-        if (!a.skip_copies) {
+        if (!block_skips(a.skip_copies)) {
             uint32_t seq = 0;   // copies into the ring so far
             int seg = 0;
             uint32_t tails = 0;
@@ -715,7 +715,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 l = 0.0f;
             }
             // a row that is left out or saw no key: zeros (m = -infinity); one
-            // that met a NaN: NaN (m = +infinity, which no other range outweighs)
+            // that met a NaN: NaN (m = +infinity, which no other range outweighs);
+            // one whose keys did not all come in time: zeros, and l = -1, which
+            // makes zeros of what it is joined with
             const bool zero = mask == 0 || (m_used == -INFINITY && l == 0.0f);
             const int64_t prow = ((int64_t)blockIdx.x * 2 + !w.at_start) * C::ROWS + t * kTileRows + r;
             const float f = zero ? 0.0f : w.whole ? 1.0f / l : 1.0f;
@@ -757,7 +759,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             }
             if (rvalid && !w.whole) {
                 a.ws_ml[prow * 2] = zero ? -INFINITY : l != l ? INFINITY : m_used;
-                a.ws_ml[prow * 2 + 1] = zero ? 0.0f : l;
+                a.ws_ml[prow * 2 + 1] = !alive ? -1.0f : zero ? 0.0f : l;
             }
             vtc::tc_fence_before();
         }
@@ -795,6 +797,7 @@ __device__ __forceinline__ void tree_join_block(const Args &a, int W) {
     const bool row_ok = rg < a.rows;
     const int cta = rg / C::ROWS, trow = rg % C::ROWS;
     float M = -INFINITY, L = 0.0f, acc[E];
+    bool lost = false;  // a partial that did not come in time is among them
 #pragma unroll
     for (int i = 0; i < E; ++i) acc[i] = 0.0f;
     if (row_ok) {
@@ -825,7 +828,10 @@ __device__ __forceinline__ void tree_join_block(const Args &a, int W) {
             }
             float mx = M;
 #pragma unroll
-            for (int k = 0; k < U; ++k) mx = fmaxf(mx, m[k]);
+            for (int k = 0; k < U; ++k) {
+                mx = fmaxf(mx, m[k]);
+                lost |= l[k] < 0.0f;
+            }
             if (mx == -INFINITY) continue;
             const float f = ex2(M - mx);
             M = mx;
@@ -844,13 +850,14 @@ __device__ __forceinline__ void tree_join_block(const Args &a, int W) {
     }
     if (W > 1) {
         part[warp][0][lane] = M;
-        part[warp][1][lane] = L;
+        part[warp][1][lane] = lost ? -1.0f : L;
 #pragma unroll
         for (int i = 0; i < E; ++i) part[warp][2 + i][lane] = acc[i];
         __syncthreads();
         if (warp % W) return;
         for (int k = 1; k < W; ++k) {
             const float m = part[warp + k][0][lane], mx = fmaxf(M, m);
+            lost |= part[warp + k][1][lane] < 0.0f;
             if (m == -INFINITY) continue;
             const float f = ex2(M - mx), wk = ex2(m - mx);
             M = mx;
@@ -861,9 +868,10 @@ __device__ __forceinline__ void tree_join_block(const Args &a, int W) {
     }
     if (!row_ok) return;
     const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
-    const float f = M == -INFINITY ? 0.0f : 1.0f / L;
+    const bool zero = lost || M == -INFINITY;
+    const float f = zero ? 0.0f : 1.0f / L;
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = M == -INFINITY ? 0.0f : acc[i] * f;
+    for (int i = 0; i < E; ++i) acc[i] = zero ? 0.0f : acc[i] * f;
     if (a.out_bf16) {
         uint32_t *dst = reinterpret_cast<uint32_t *>((uint16_t *)a.out + orow * D + lane * E);
 #pragma unroll
