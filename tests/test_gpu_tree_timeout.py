@@ -101,3 +101,22 @@ def test_every_other_block_without_copies(fault, n_q, hq, d, requests, longest):
     st, out = c.run()
     assert st == 0 and torch.equal(out, clean)
     check_attn(out, c.hf, c.qn, c.masks[0], float(np.float32(d ** -0.5)), 0)
+
+
+@pytest.mark.parametrize("n_q,hq", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_copy_at_all(fault, n_q, hq, d, dtype):
+    """20 and 40 nodes of 14 heads are two and three tiles; one tile (Q in TMEM,
+    two blocks to an SM) takes 16 of them or fewer."""
+    c = Call(n_q, hq, d, [n_q, 3000, 900], dtype)
+    st, clean = c.run()
+    assert st == 0
+    for b in range(3):
+        check_attn(clean, c.hf, c.qn, c.masks[b], float(np.float32(d ** -0.5)), b)
+    fault(20_000, 1)
+    st, out = c.run()
+    assert st == TIMEOUT and bool((out == 0).all())
+    fault(0, 0)
+    st, out = c.run()
+    assert st == 0 and torch.equal(out, clean)
