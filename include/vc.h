@@ -739,9 +739,11 @@ VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t ro
  * wait on a copy runs into the limit: attention outputs are then zeros and
  * nothing of the cache is read; log probabilities are as vc_token_logprobs
  * says.  skip_copies == 2: of a tree-attention or token-log-probability
- * launch only the blocks of odd index do so.  Calls racing with launches on
- * other threads see either setting.  VC_ERR_INVALID_ARG for a limit out of
- * range.
+ * launch only the blocks of odd index do so.  A short limit with skip_copies
+ * == 0 is for these two alone, whose blocks end after the copies that they
+ * issued: those of the other kernels do not wait for them once a wait has run
+ * out.  Calls racing with launches on other threads see either setting.
+ * VC_ERR_INVALID_ARG for a limit out of range.
  */
 VC_API vc_status vc_debug_set_wait_fault(int64_t wait_limit_ns, int32_t skip_copies);
 

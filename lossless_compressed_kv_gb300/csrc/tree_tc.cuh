@@ -107,7 +107,7 @@ struct Cfg {
     static constexpr int OFF_STAGE = OFF_KV + SLOTS * SLOT;
     static constexpr int OFF_BAR = OFF_STAGE + STAGE;
     static constexpr int NS = NBUF < QT ? QT : NBUF;  // S barriers: by buffer, or by tile
-    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 1;  // q, o, pv per tile; s; p per buffer; full, empty; tail
+    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 2;  // q, o, pv per tile; s; p per buffer; full, empty; tail, idle
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM = OFF_MISC + kBadRing * 8 + 16;
     static_assert(SMEM <= (QT == 1 ? 113 : 227) * 1024, "shared memory of the CTAs an SM holds");
@@ -321,6 +321,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
     uint64_t *q_ready = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [QT]
     uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + C::NS, *o_done = p_ready + C::NBUF, *pv_done = o_done + QT;
     uint64_t *full = pv_done + QT, *empty = full + C::SLOTS, *tail = empty + C::SLOTS;
+    uint64_t *idle = tail + 1;
     unsigned long long *bad = reinterpret_cast<unsigned long long *>(smem + C::OFF_MISC);  // [kBadRing]
     uint32_t *tslot = reinterpret_cast<uint32_t *>(bad + kBadRing);
 
@@ -344,6 +345,7 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
             mbar_init(&empty[i], 1);
         }
         mbar_init(tail, 1);
+        mbar_init(idle, 1);
         fence_mbar_init();
     }
     if (warp == 0) {
@@ -477,11 +479,12 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 ++seg;
             }
             flush();
-            // no copy may be under way when the CTA ends
+            // no copy may be under way when the CTA ends (however short the limit of
+            // the waits before)
             for (uint32_t q = seq > C::SLOTS ? seq - C::SLOTS : 0; q < seq; ++q)
-                if ((int)(q % C::SLOTS) != lost &&
-                    !mbar_wait(&full[q % C::SLOTS], (q / C::SLOTS) & 1, a.status, a.wait_ns))
+                if ((int)(q % C::SLOTS) != lost && !mbar_wait(&full[q % C::SLOTS], (q / C::SLOTS) & 1, a.status, kWaitNs))
                     break;
+            if (lost >= 0) mbar_wait(tail, (tails - 1) & 1, a.status, kWaitNs);
         }
     } else if (warp == C::SM_WARPS + 1) {
         // ================= MMA issue (the warp in step, one elected thread) =================
@@ -573,6 +576,9 @@ __device__ __forceinline__ void tree_cta(const Args &a, uint8_t *smem) {
                 vp.step(2, C::SLOTS);
             }
         }
+        // nor may a product be: TMEM is freed behind it
+        umma_commit(idle);
+        mbar_wait(idle, 0, a.status, kWaitNs);
     } else if (QT > 1 && warp >= C::SM_WARPS) {
         // (idle warps of that warpgroup)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));

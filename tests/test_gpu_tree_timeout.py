@@ -120,3 +120,22 @@ def test_no_copy_at_all(fault, n_q, hq, d, dtype):
     fault(0, 0)
     st, out = c.run()
     assert st == 0 and torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("n_q,hq", KERNELS)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("requests", [1, 40])
+def test_a_limit_that_runs_out_while_copies_are_under_way(fault, n_q, hq, d, requests):
+    """Each row is whole or zeros, and blocks end after their copies and products."""
+    rng = np.random.default_rng(requests)
+    c = Call(n_q, hq, d, [int(x) for x in rng.integers(n_q, 4000, requests)], torch.float32)
+    _, clean = c.run()
+    fault(1, 0)
+    for _ in range(3):
+        st, out = c.run()
+        got, want = c.rows(out), c.rows(clean)
+        zero, same = (got == 0).all(-1), (got == want).all(-1)
+        assert bool((zero ^ same).all()) and (st == TIMEOUT or not bool(zero.any()))
+    fault(0, 0)
+    st, out = c.run()
+    assert st == 0 and torch.equal(out, clean)
