@@ -97,3 +97,42 @@ def test_commits_after_rebound_lengths_and_tables():
         kv.k_pages, kv.v_pages = (torch.cat([p, p[:3]]) for p in (kv.k_pages, kv.v_pages))
     gc.collect()
     step(layers, lens[:2], paths[:2])
+
+
+def test_refused_requests_keep_both_pools():
+    rng = np.random.default_rng(1)
+    n_q, hkv, d = 6, 2, 64
+    lens = np.array([20, 20, 20, 5, 20, 20, 20], np.int32)
+    kvs, _ = layers_of(rng, np.maximum(lens, 20), hkv, d, 2)
+    kvs[0].seq_lens.copy_(H.to_dev(lens))
+    good = [0, 2, 5, -1, -1, -1]
+    pa = H.to_dev(np.array([good, [0, 3, 2, -1, -1, -1], [0, 2, 6, -1, -1, -1], good, [1, 2, 5, -1, -1, -1], good, good],
+                           np.int32))
+    before = [(kv.k_pages.clone(), kv.v_pages.clone()) for kv in kvs]
+    layers = vc().KVLayers(kvs)
+    for only, a in enumerate([2, 2, 2, 2, 6, -2], 1):
+        al = np.full(7, -1, np.int32)
+        al[only] = a
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        vc().tree_commit(layers, H.to_dev(al), pa, status=st)
+        torch.cuda.synchronize()
+        assert st.item() == 3, only
+        for kv, (k, v) in zip(kvs, before):
+            assert torch.equal(kv.k_pages, k) and torch.equal(kv.v_pages, v), only
+
+
+@pytest.mark.parametrize("page", [-1, 1 << 20, "count"])
+@pytest.mark.parametrize("column,skipped", [(0, [(0, 1)]), (1, [(0, 1), (0, 2), (0, 3)]), (2, [(0, 3)])])
+def test_a_bad_page_stops_its_entries_alone(page, column, skipped):
+    """The tree of request 0 lies in positions 14 to 35, its path's moves are 16
+    -> 15, 20 -> 16 and 33 -> 17: a bad page of either end stops a move, the
+    others and the other requests are served."""
+    rng = np.random.default_rng(2)
+    n_q, hkv, d, lens = 22, 2, 64, np.array([36, 50, 36], np.int32)
+    kvs, table = layers_of(rng, lens, hkv, d, 2)
+    paths = [[0, 2, 6, 19], [0, 4, 21], [0, 1, 3]]
+    kvs[0].block_table[0, column] = kvs[0].num_pages if page == "count" else page
+    want = [[moved(p, table, hkv, d, lens, n_q, paths, skipped) for p in (kv.k_pages, kv.v_pages)] for kv in kvs]
+    assert commit(vc().KVLayers(kvs), paths, n_q) == 3
+    for kv, (k, v) in zip(kvs, want):
+        assert torch.equal(kv.k_pages, k) and torch.equal(kv.v_pages, v)
