@@ -495,6 +495,13 @@ def _here(name: str, t, dev: int):
     return t.data_ptr()
 
 
+def _room(workspace, dev: int):
+    """Address and size of a workspace, all of whose bytes are its own."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return _here("workspace", workspace, dev), workspace.nbytes
+
+
 def _status(status, dev: int):
     return None if status is None else _need("status", status, _I32, (1,), dev)
 
@@ -591,7 +598,7 @@ def tree_attn(q, full: PagedKV, mask, softmax_scale: float, out, max_seq_len: in
     _check(_lib.vc_tree_attn(
         _need("q", q, _BF16, shape, dev), n_q, hq, C.byref(fs), _need("mask", mask, _I64, (b, n_q), dev), softmax_scale,
         _need("out", out, out.dtype, shape, dev), _DTYPES.get(out.dtype, -1), max_seq_len,
-        _here("workspace", workspace, dev), workspace.nbytes, _status(status, dev), _on(stream, dev)), "vc_tree_attn")
+        *_room(workspace, dev), _status(status, dev), _on(stream, dev)), "vc_tree_attn")
 
 
 def tree_accept(parent, tokens, verified, accept_len, path, emitted, stream=None):
@@ -680,7 +687,7 @@ def token_logprobs(logits, ids, logprobs, workspace, temperature: float = 1.0, e
         _need("ids", ids, _I32, (rows, n_ids), dev), n_ids, temperature, k,
         _need("logprobs", logprobs, _F32, (rows, n_ids), dev),
         None if entropy is None else _need("entropy", entropy, _F32, (rows,), dev), ti, tl,
-        _here("workspace", workspace, dev), workspace.nbytes, _status(status, dev), _on(stream, dev)),
+        *_room(workspace, dev), _status(status, dev), _on(stream, dev)),
         "vc_token_logprobs")
 
 

@@ -191,3 +191,23 @@ def test_wrappers_refuse_halves(vc):
         vc.token_logprobs(x, i, x[:, :1], x, top_ids=i)
     with pytest.raises(ValueError, match="come together"):
         vc.token_logprobs(x, i, x[:, :1], x, top_logprobs=x[:, :1])
+
+
+def test_wrappers_refuse_workspaces_of_fewer_bytes_than_they_count(vc, monkeypatch):
+    """A broadcast workspace has one element's memory, whatever its shape says."""
+    monkeypatch.setattr(vc, "_device", lambda: -1)          # where CPU tensors are
+    monkeypatch.setattr(vc, "_on", lambda stream, dev: None)
+    class NotReached:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(name)
+
+    monkeypatch.setattr(vc, "_lib", NotReached())
+    wide = torch.zeros(1, dtype=torch.uint8).expand(1 << 40)
+    one, m = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 4), dtype=torch.int64)
+    kv = vc.PagedKV(torch.zeros((2, 4096), dtype=torch.uint8), torch.zeros((2, 4096), dtype=torch.uint8),
+                    torch.zeros((2, 1), dtype=torch.int32), one, 1, 128, 16)
+    q = torch.zeros((2, 4, 1, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="workspace"):
+        vc.tree_attn(q, kv, m, 1.0, torch.zeros_like(q), 16, wide)
+    with pytest.raises(ValueError, match="workspace"):
+        vc.token_logprobs(torch.zeros((2, 8)), one.view(2, 1), torch.zeros((2, 1)), wide)
