@@ -559,8 +559,12 @@ VC_API vc_status vc_rope_kv_write(const float *qkv, int32_t m, const int32_t *ro
  *                      frequency, pairs that do not complete low_turns are
  *                      stretched by s, those between are blended)
  * factor 1 leaves f_i = w_i.  f_i / 2pi is kept as a 64-bit binary fraction and
- * multiplied by the position modulo 1: an angle is off by at most 2^-32 of a
- * turn for positions below 2^22 (2^-24 of a turn at 2^31).
+ * multiplied by the position modulo 1 in integers: that fraction of a turn is
+ * off by at most 2^-32 + pos 2^-55.  The angle in radians made of it in fp32 is
+ * off by less than 2^-21 more (a conversion, a constant and a product, each
+ * rounded), and its sine and cosine by less than 2^-21 again.  The fields are
+ * fp32, and what fp32 does not hold is rounded first: a factor of 1.3 by 2^-25
+ * of itself, which turns position 131072 by 0.004 radians.
  */
 typedef struct {
     float theta;          /* >= 1                                         */

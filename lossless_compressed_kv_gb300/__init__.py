@@ -534,7 +534,7 @@ class Rotary:
     """Rotary positions (vc_rotary in include/vc.h): base theta, the first
     rot_dim channels of a head, half or interleaved pairs, and frequencies
     stretched by factor (all of them, or by how often a pair turns within
-    original_len)."""
+    original_len).  The numbers are rounded to fp32."""
     theta: float
     rot_dim: int
     interleaved: bool = False

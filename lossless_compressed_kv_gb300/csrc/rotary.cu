@@ -35,8 +35,10 @@ struct RotArgs {
 
 // cos and sin (times the amplitude) of pair i at a position.  The fraction of
 // a turn as a signed 32-bit number of 2^-32 turns, so the angle lies in
-// [-pi, pi], where the fast sine and cosine are off by at most 2^-21: the
-// result is rounded to bf16, whose half step is 2^-8 of the value.
+// [-pi, pi].  Its conversion to fp32 rounds by up to 2^-26 turn (0.94e-7
+// radians), the constant and the product by 2^-24 pi and 2^-23 more: 4e-7 in
+// all, below 2^-21; the fast sine and cosine are off by at most 2^-21 there.
+// The result is rounded to bf16, whose half step is 2^-8 of the value.
 __device__ inline float2 cos_sin(uint64_t turns, int pos, float amp) {
     const int32_t frac = (int32_t)((turns * (uint64_t)(uint32_t)pos) >> 32);
     float s, c;

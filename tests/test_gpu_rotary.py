@@ -191,3 +191,25 @@ def test_agrees_with_rope_kv_write_near_the_start():
     for a, b in zip(out[0][:2], out[1][:2]):
         assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 12 * 64 * 2.0 ** -23).all()
     assert torch.equal(out[0][2], out[1][2])
+
+
+@pytest.mark.parametrize("factor", [1.0, 1.5, 8.0])
+def test_the_angle_is_as_exact_as_stated(factor):
+    """Where a sine or cosine is next to zero bf16 has digits to spare.  Off by
+    at most 2^-21 (angle) + 2^-21 (sine, cosine) + half a bf16 step; the far
+    positions' share (2^22 2^-55 turns) and the product with 1 add below 2^-28."""
+    pos = np.arange(1 << 22)
+    t = pos / factor
+    near = np.concatenate([np.argsort(np.abs(f(t)))[:400] for f in (np.sin, np.cos)] + [pos[-100:]])
+    p = H.to_dev(near.astype(np.int32))
+    n = len(near)
+    qkv = torch.zeros((n, 3 * 32), device="cuda")
+    qkv[:, 0] = 1.0
+    kv = vc().PagedKV.allocate(n // 16 + 1, 1, 32, 16, torch.arange(n // 16 + 1, dtype=torch.int32, device="cuda")[None],
+                               torch.zeros(1, dtype=torch.int32, device="cuda"), zero=True)
+    q = torch.zeros((n, 1, 32), dtype=torch.bfloat16, device="cuda")
+    vc().rotary_kv_write(qkv, torch.zeros_like(p), p, 1, vc().Rotary(1e4, 2, factor=factor), q, kv,
+                         row_slot=torch.arange(n, dtype=torch.int32, device="cuda"))
+    got = q[:, 0, :2].double().cpu().numpy()
+    want = np.stack([np.cos(t[near]), np.sin(t[near])], 1)
+    assert (np.abs(got - want) <= 2.0 ** -20 + 2.0 ** -28 + 2.0 ** -8 * np.abs(want)).all()
