@@ -710,7 +710,8 @@ VC_API vc_status vc_tree_commit(const vc_paged_kv *layers, int32_t n_layers, int
  *  top_ids       device int32 [rows][top_k], 0 <= top_k <= 64: the ids of the
  *                largest logits in falling order, equal logits by lower id.
  *                Logits of -infinity are not listed: -1 fills the rest
- *  top_logprobs  device fp32 [rows][top_k], -infinity beside a -1
+ *  top_logprobs  device fp32 [rows][top_k], -infinity beside a -1 (with more
+ *                than 32 alternatives a row may be read again once for each)
  *  workspace     vc_token_logprobs_workspace_bytes(rows, vocab, top_k) bytes,
  *                8-byte aligned (calls that may run at the same time take one
  *                each)

@@ -47,7 +47,16 @@
 // has arrived, before it is handed on, and notes the nodes; rows that do see
 // one of those end as NaN.
 //
-// Every wait is bounded; a timeout is reported and the CTA drains.
+// Rounding.  P enters the second product in bf16, whatever the output's type:
+// an MMA takes operands of one type, and V is bf16 (P as a sum of two bf16
+// numbers would double the products of P V).  Each probability is off by at
+// most half a step, 2^-8 of itself; together that is 0.0012 (64 keys) to 0.0017
+// (4096 and more) of a result's norm, as much as a bf16 output's own rounding,
+// and 0.0023 with it.  Scores, maxima, sums and O are fp32; the sum takes P as
+// it is before rounding.
+//
+// Every wait is bounded.  A timeout is reported and the CTA drains: its rows of
+// one range are zeros, and so are those joined with one of its partials.
 #pragma once
 
 #include "verify_tc.cuh"
