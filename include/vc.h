@@ -732,6 +732,93 @@ VC_API vc_status vc_token_logprobs(const void *logits, int32_t dtype, int32_t ro
                                    int32_t *dev_status, vc_stream_t stream);
 
 /*
+ * A cache held in 8 bits, with one scale for each block of a page (16 tokens)
+ * and kv head, for K and for V: value = scale * code.  A draft cache that is
+ * nearly lossless at half the bytes of KV_full.  Entry j of request b is
+ * position j of KV_full.  The pools' pages are those of vc_paged_kv, a byte a
+ * value.
+ *  e4m3  8-bit floats, largest value 448; codes 0x7f and 0xff (NaN) make the
+ *        results void of every row of their request and kv head
+ *  int8  -127 .. 127
+ * Scales are numbers from 2^-126 to 2^122; others count as the nearer end.
+ */
+typedef enum { VC_E4M3 = 0, VC_INT8 = 1 } vc_code8;
+typedef struct {
+    void *k_codes;              /* device [num_pages][num_kv_heads][16][head_dim] */
+    void *v_codes;
+    float *k_scales;            /* device [num_pages][num_kv_heads]               */
+    float *v_scales;
+    int64_t num_pages;
+    const int32_t *block_table; /* device int32 [batch][max_blocks]               */
+    const int32_t *seq_lens;    /* device int32 [batch]                           */
+    int32_t batch;
+    int32_t max_blocks;
+    int32_t num_kv_heads;       /* >= 1                                           */
+    int32_t head_dim;           /* 64 or 128                                      */
+    int32_t code;               /* vc_code8                                       */
+} vc_paged_kv8;
+
+/*
+ * vc_kv8_write -- make the 8-bit pages that hold positions first[b] ..
+ * full->seq_lens[b] - 1 anew from KV_full.  A block's scale follows its
+ * largest magnitude, so a page with a new token is made again whole, from the
+ * values and not from its old codes: a page's content depends on the rows of
+ * KV_full alone, however its tokens came.  Per block x of a page and kv head
+ * (fp32, each operation rounded to nearest even):
+ *   top = 448 (e4m3) or 127 (int8)
+ *   scale = max(max |x| * fp32(1 / top), 2^-126),  r = 1 / scale
+ *   code = x * r, limited to [-top, top], rounded to nearest even
+ * Slots behind the last token get code 0.  Infinities take no part in the
+ * scale and get the largest code, NaN code 0; either is reported
+ * (VC_ERR_INVALID_ARG in dev_status).
+ *  full         bits == 16, head_dim 64 or 128; pools on 16-byte boundaries
+ *  first        device int32 [batch] or NULL (= 0): the first new position;
+ *               pages before its own are not touched (first[b] >=
+ *               seq_lens[b]: none is)
+ *  dst          same batch, heads and head_dim; seq_lens is not read; codes
+ *               on 16-byte boundaries
+ *  max_seq_len  host: bound of every full->seq_lens[b] (grid size)
+ * A request with a negative first or length, or one above max_seq_len, is
+ * left out and reported (VC_ERR_BAD_INDEX), a page out of range likewise.
+ */
+VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, const vc_paged_kv8 *dst,
+                              int32_t max_seq_len, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_kv8_attn -- attention over an 8-bit cache: request b holds seq_lens[b]
+ * tokens, the last n_q of which are a block of queries.  n_q = 1 is a drafting
+ * step.
+ *   out[i] = sum_t softmax_t(scale <q_i, sk_t ck_t>) sv_t cv_t
+ *  q            device bf16 [batch][n_q][num_q_heads][head_dim], finite
+ *  mask         NULL: query i attends to the tokens before the block and to
+ *               those of the block up to itself.  Else device uint64
+ *               [batch][n_q] as in vc_tree_attn: to the tokens before the
+ *               block and to those whose bit is set; 0 leaves the row out:
+ *               zeros.
+ *  out          device [batch][n_q][num_q_heads][head_dim], out_dtype VC_F32
+ *               or VC_BF16
+ *  max_seq_len  host: bound of every seq_lens[b]
+ *  workspace    vc_kv8_workspace_bytes, on a 32-byte boundary (calls that may
+ *               run at the same time take one each)
+ * 1 <= n_q <= 64, num_q_heads / num_kv_heads <= 8, softmax_scale > 0; codes, q
+ * and out on 16-byte boundaries.  A request with seq_lens[b] = 0 is idle: zeros.
+ * One with fewer than n_q tokens, or more than max_seq_len or max_blocks
+ * pages, gets zeros and VC_ERR_BAD_INDEX; a row whose keys did not all arrive
+ * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT.
+ * Codes are exact in the products' type (fp16), and q is taken times a power
+ * of two for each row that fits it there; probabilities enter the second product in fp16
+ * (each off by at most 2^-11 of itself, or 2^-25 of the largest beside V's
+ * largest scale).  Everything else is fp32.  The context is split evenly over
+ * the GPU, so the last bits of a result depend on the batch's lengths; they
+ * are the same from call to call.
+ */
+VC_API size_t vc_kv8_workspace_bytes(const vc_paged_kv8 *kv, int32_t n_q, int32_t num_q_heads, int32_t max_seq_len);
+VC_API vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_paged_kv8 *kv,
+                             const uint64_t *mask, float softmax_scale, void *out, int32_t out_dtype,
+                             int32_t max_seq_len, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                             vc_stream_t stream);
+
+/*
  * vc_debug_set_wait_fault -- fault injection for tests of the bounded device
  * waits (host-side switch, process-wide, off by default; not for production
  * use).  Every wait of a kernel on a copy or on another warp gives up after

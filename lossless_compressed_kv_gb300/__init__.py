@@ -51,6 +51,12 @@ class PagedKVStruct(C.Structure):
                 ("max_blocks", C.c_int32), ("fmt", KVFormat)]
 
 
+class PagedKV8Struct(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_scales", C.c_void_p),
+                ("num_pages", C.c_int64), ("block_table", C.c_void_p), ("seq_lens", C.c_void_p), ("batch", C.c_int32),
+                ("max_blocks", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("code", C.c_int32)]
+
+
 class RotaryStruct(C.Structure):
     _fields_ = [("theta", C.c_float), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("factor", C.c_float),
                 ("original_len", C.c_int32), ("low_turns", C.c_float), ("high_turns", C.c_float),
@@ -116,6 +122,10 @@ _SIG = {
     "vc_token_logprobs_workspace_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32]),
     "vc_token_logprobs": (C.c_int, [_P, C.c_int32, C.c_int32, C.c_int32, C.c_int64, _P, C.c_int32, C.c_float,
                                     C.c_int32, _P, _P, _P, _P, _P, C.c_size_t, _P, _P]),
+    "vc_kv8_write": (C.c_int, [C.POINTER(PagedKVStruct), _P, C.POINTER(PagedKV8Struct), C.c_int32, _P, _P]),
+    "vc_kv8_workspace_bytes": (C.c_size_t, [C.POINTER(PagedKV8Struct), C.c_int32, C.c_int32, C.c_int32]),
+    "vc_kv8_attn": (C.c_int, [_P, C.c_int32, C.c_int32, C.POINTER(PagedKV8Struct), _P, C.c_float, _P, C.c_int32,
+                              C.c_int32, _P, C.c_size_t, _P, _P]),
     "vc_draft_attn_static": (C.c_int, [_P, C.c_int32, C.POINTER(PagedKVStruct), C.c_float, _P, C.c_int32, _P, _P]),
     "vc_static_scratch_bytes": (C.c_size_t, []),
     "vc_stagger_plan": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P]),
@@ -689,6 +699,105 @@ def token_logprobs(logits, ids, logprobs, workspace, temperature: float = 1.0, e
         None if entropy is None else _need("entropy", entropy, _F32, (rows,), dev), ti, tl,
         *_room(workspace, dev), _status(status, dev), _on(stream, dev)),
         "vc_token_logprobs")
+
+
+# ---------------------------------------------------------------------------
+# a cache held in 8 bits
+# ---------------------------------------------------------------------------
+
+_CODES8 = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_PAGED_KV8 = struct.Struct("PPPPqPPiiiii4x").pack   # PagedKV8Struct
+
+
+@dataclass
+class PagedKV8:
+    """A paged K/V cache in 8 bits (vc_paged_kv8 in include/vc.h).
+
+    k_codes / v_codes: float8_e4m3fn or int8 device tensors [num_pages,
+    num_kv_heads, 16, head_dim]; k_scales / v_scales: fp32 [num_pages,
+    num_kv_heads], value = scale * code; block_table: int32 [batch,
+    max_blocks]; seq_lens: int32 [batch]."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_scales: torch.Tensor
+    block_table: torch.Tensor
+    seq_lens: torch.Tensor
+
+    @property
+    def batch(self) -> int:
+        return int(self.block_table.shape[0])
+
+    @property
+    def num_pages(self) -> int:
+        return int(self.k_codes.shape[0])
+
+    @property
+    def num_kv_heads(self) -> int:
+        return int(self.k_codes.shape[1])
+
+    @property
+    def head_dim(self) -> int:
+        return int(self.k_codes.shape[3])
+
+    @staticmethod
+    def allocate(num_pages: int, num_kv_heads: int, head_dim: int, code: torch.dtype, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, device="cuda") -> "PagedKV8":
+        codes = [torch.zeros((num_pages, num_kv_heads, PAGE, head_dim), dtype=torch.uint8, device=device).view(code)
+                 for _ in range(2)]
+        scales = [torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return PagedKV8(*codes, *scales, block_table, seq_lens)
+
+
+def _cache8(kv: PagedKV8, dev: int) -> PagedKV8Struct:
+    """The struct of an 8-bit cache whose six tensors are contiguous on device dev."""
+    k, table = kv.k_codes, kv.block_table
+    shape, dtype = k.shape, k.dtype
+    n, hkv, page, d = shape
+    if page != PAGE:
+        raise ValueError("codes must be [num_pages][num_kv_heads][16][head_dim]")
+    b, w = table.shape
+    return PagedKV8Struct.from_buffer_copy(_PAGED_KV8(
+        _need("k_codes", k, dtype, shape, dev), _need("v_codes", kv.v_codes, dtype, shape, dev),
+        _need("k_scales", kv.k_scales, _F32, (n, hkv), dev), _need("v_scales", kv.v_scales, _F32, (n, hkv), dev), n,
+        _need("block_table", table, _I32, (b, w), dev), _need("seq_lens", kv.seq_lens, _I32, (b,), dev), b, w, hkv, d,
+        _CODES8.get(dtype, -1)))
+
+
+def kv8_write(full: PagedKV, first, kv8: PagedKV8, max_seq_len: int, status=None, stream=None):
+    """vc_kv8_write: make the 8-bit pages that hold positions first[b] (int32
+    [B]; None: 0) to full.seq_lens[b] - 1 anew from KV_full."""
+    dev = _device()
+    fs, ds = _cache(full, dev), _cache8(kv8, dev)
+    _check(_lib.vc_kv8_write(
+        C.byref(fs), None if first is None else _need("first", first, _I32, (fs.batch,), dev), C.byref(ds),
+        max_seq_len, _status(status, dev), _on(stream, dev)), "vc_kv8_write")
+
+
+def kv8_workspace_bytes(kv8: PagedKV8, n_q: int, num_q_heads: int, max_seq_len: int) -> int:
+    s = PagedKV8Struct(num_pages=kv8.num_pages, batch=kv8.batch, max_blocks=int(kv8.block_table.shape[1]),
+                       num_kv_heads=kv8.num_kv_heads, head_dim=kv8.head_dim, code=_CODES8.get(kv8.k_codes.dtype, -1))
+    return int(_lib.vc_kv8_workspace_bytes(C.byref(s), int(n_q), int(num_q_heads), int(max_seq_len)))
+
+
+def kv8_attn(q, kv8: PagedKV8, softmax_scale: float, out, max_seq_len: int, workspace, mask=None, status=None,
+             stream=None):
+    """vc_kv8_attn: q bf16 [B][n_q][Hq][D] (or [B][Hq][D]: one token each)
+    over an 8-bit cache whose last n_q tokens are the block; causal in the
+    block, or by mask (int64 [B][n_q], of tree_plan); out fp32 or bf16 of q's
+    shape."""
+    shape = q.shape
+    b, hq, d = shape[0], shape[-2], shape[-1]
+    n_q = shape[1] if len(shape) == 4 else 1
+    if len(shape) not in (3, 4) or b != kv8.block_table.shape[0] or d != kv8.k_codes.shape[3]:
+        raise ValueError("q must be [batch][n_q][num_q_heads][head_dim] of the cache")
+    dev = _device()
+    ks = _cache8(kv8, dev)
+    _check(_lib.vc_kv8_attn(
+        _need("q", q, _BF16, shape, dev), n_q, hq, C.byref(ks),
+        None if mask is None else _need("mask", mask, _I64, (b, n_q), dev), softmax_scale,
+        _need("out", out, out.dtype, shape, dev), _DTYPES.get(out.dtype, -1), max_seq_len, *_room(workspace, dev),
+        _status(status, dev), _on(stream, dev)), "vc_kv8_attn")
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,147 @@
+// vc_kv8_attn: attention over a cache held in 8 bits (see kv8.cuh).
+#include <cmath>
+
+#include "kv8_few.cuh"
+
+namespace vc {
+bool encode_pool8(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d);
+namespace {
+
+template <int D, int NT, bool E4M3>
+__global__ void __launch_bounds__(kv8::Few<D, NT>::THREADS, kv8::Few<D, NT>::CTAS)
+    kv8_few_kernel(const __grid_constant__ kv8::Args a) {
+    pdl_wait();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    kv8::few_warp<D, NT, E4M3>(a, smem);
+    pdl_trigger();
+}
+
+template <int D, int BK>
+__global__ void __launch_bounds__(kv8::kJoinWarps * 32)
+    kv8_join_kernel(const __grid_constant__ kv8::Args a, int warps_per_row, int lane_rows) {
+    pdl_begin();
+    kv8::join_block<D, BK>(a, warps_per_row, lane_rows);
+}
+
+bool supported(const vc_paged_kv8 &kv, int n_q, int hq) {
+    const int d = kv.head_dim, hkv = kv.num_kv_heads;
+    return (kv.code == VC_E4M3 || kv.code == VC_INT8) && (d == 64 || d == 128) && hkv >= 1 && hq >= hkv &&
+           hq % hkv == 0 && hq / hkv <= VC_MAX_GQA_GROUP && n_q >= 1 && n_q <= VC_MAX_VERIFY_QUERIES;
+}
+
+// How a call is laid out over the GPU.
+struct Plan {
+    int nt;                         // eights of rows of a warp
+    int lanes, lane_rows, groups;   // chunks of rows, their rows, ranges of the context
+    int64_t slots() const { return (int64_t)groups * lanes * 2 * lane_rows; }  // partial rows
+};
+Plan plan_of(const vc_paged_kv8 &kv, int n_q, int hq, int max_seq_len) {
+    const int rows = n_q * (hq / kv.num_kv_heads);
+    Plan p;
+    p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    p.lane_rows = 8 * p.nt;
+    p.lanes = ceil_div(rows, p.lane_rows);
+    const int64_t pages = (int64_t)kv.batch * kv.num_kv_heads * ceil_div(max_seq_len, kPage);
+    const int most = tree::kSMs * 4 * (p.nt == 1 ? 4 : p.nt == 2 ? 3 : 2);
+    p.groups = (int)(pages < 1 ? 1 : pages < most ? pages : most);
+    return p;
+}
+size_t workspace_of(const Plan &p, int d) { return (size_t)p.slots() * (d + 2) * sizeof(float); }
+
+template <int D, int NT, bool E4M3>
+cudaError_t launch_few(const kv8::Args &a, cudaStream_t st) {
+    using F = kv8::Few<D, NT>;
+    cudaError_t e = set_smem_limit((const void *)kv8_few_kernel<D, NT, E4M3>, F::SMEM);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kv8_few_kernel<D, NT, E4M3>, dim3(ceil_div(a.groups, F::WARPS), a.lanes), F::THREADS, F::SMEM, st, a);
+    if (e != cudaSuccess) return e;
+    // ranges that a unit spans, were the lengths alike: a warp reads eight at once
+    const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
+    const dim3 grid(a.batch * a.hkv, ceil_div(a.rows, kv8::kJoinWarps / W));
+    e = launch_pdl(kv8_join_kernel<D, kPage>, grid, kv8::kJoinWarps * 32, 0, st, a, W, F::ROWS);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <int D, bool E4M3>
+cudaError_t launch(const Plan &p, const kv8::Args &a, cudaStream_t st) {
+    return p.nt == 1 ? launch_few<D, 1, E4M3>(a, st) : p.nt == 2 ? launch_few<D, 2, E4M3>(a, st) : launch_few<D, 4, E4M3>(a, st);
+}
+
+}  // namespace
+
+// The sizes of an 8-bit cache, and its pointers.
+bool kv8_sizes_ok(const vc_paged_kv8 *p) {
+    return p && p->batch >= 0 && p->num_kv_heads >= 1 && p->head_dim >= 1 && p->num_pages >= 0;
+}
+bool kv8_ok(const vc_paged_kv8 *p) {
+    return p->k_codes && p->v_codes && p->k_scales && p->v_scales && p->block_table && p->max_blocks >= 1 &&
+           p->num_pages >= 1 && !((uintptr_t)p->k_codes & 15) && !((uintptr_t)p->v_codes & 15) &&
+           !((uintptr_t)p->k_scales & 3) && !((uintptr_t)p->v_scales & 3);
+}
+
+}  // namespace vc
+
+using namespace vc;
+
+extern "C" {
+
+size_t vc_kv8_workspace_bytes(const vc_paged_kv8 *kv, int32_t n_q, int32_t num_q_heads, int32_t max_seq_len) {
+    if (!kv8_sizes_ok(kv) || max_seq_len < 0 || !supported(*kv, n_q, num_q_heads)) return 0;
+    return workspace_of(plan_of(*kv, n_q, num_q_heads, max_seq_len), kv->head_dim);
+}
+
+vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_paged_kv8 *kv, const uint64_t *mask,
+                      float softmax_scale, void *out, int32_t out_dtype, int32_t max_seq_len, void *workspace,
+                      size_t workspace_bytes, int32_t *dev_status, vc_stream_t stream) {
+    if (!kv8_sizes_ok(kv) || max_seq_len < 0 || n_q < 1 || !(softmax_scale > 0.0f) || !std::isfinite(softmax_scale))
+        return VC_ERR_INVALID_ARG;
+    const float scale_log2 = softmax_scale * 1.4426950408889634f;
+    if (!supported(*kv, n_q, num_q_heads) || (out_dtype != VC_F32 && out_dtype != VC_BF16) || !std::isfinite(scale_log2))
+        return VC_ERR_UNSUPPORTED;
+    // (the kernels count pages, and the rows of a pool, in 32 bits)
+    const int64_t held = (int64_t)kv->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
+    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX ||
+        kv->num_pages > INT32_MAX / kPage / kv->num_kv_heads)
+        return VC_ERR_UNSUPPORTED;
+    if (kv->batch == 0) return VC_OK;
+    if (!q || !out || !kv8_ok(kv) || !kv->seq_lens || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 31))
+        return VC_ERR_INVALID_ARG;
+    const Plan p = plan_of(*kv, n_q, num_q_heads, max_seq_len);
+    const int d = kv->head_dim;
+    if (!workspace || workspace_bytes < workspace_of(p, d)) return VC_ERR_WORKSPACE;
+    kv8::Args a;
+    a.ks = kv->k_scales;
+    a.vs = kv->v_scales;
+    a.q = (const uint16_t *)q;
+    a.n_pages = kv->num_pages;
+    a.table = kv->block_table;
+    a.lens = kv->seq_lens;
+    a.mask = (const unsigned long long *)mask;
+    a.batch = kv->batch;
+    a.maxb = kv->max_blocks;
+    a.n_q = n_q;
+    a.hq = num_q_heads;
+    a.hkv = kv->num_kv_heads;
+    a.grp = num_q_heads / a.hkv;
+    a.max_len = (int)longest;
+    a.rows = n_q * a.grp;
+    a.lanes = p.lanes;
+    a.groups = p.groups;
+    a.scale_log2 = scale_log2;
+    a.ws_o = (float *)workspace;
+    a.ws_ml = a.ws_o + (size_t)p.slots() * d;
+    a.out = out;
+    a.out_bf16 = out_dtype == VC_BF16;
+    a.status = dev_status;
+    a.wait_ns = wait_fault().wait_ns;
+    a.skip_copies = wait_fault().skip_copies;
+    if (!encode_pool8(&a.kmap, kv->k_codes, kv->num_pages, a.hkv, d) ||
+        !encode_pool8(&a.vmap, kv->v_codes, kv->num_pages, a.hkv, d))
+        return VC_ERR_CUDA;
+    const cudaStream_t st = (cudaStream_t)stream;
+    const bool e4m3 = kv->code == VC_E4M3;
+    const cudaError_t e = d == 64 ? (e4m3 ? launch<64, true>(p, a, st) : launch<64, false>(p, a, st))
+                                  : (e4m3 ? launch<128, true>(p, a, st) : launch<128, false>(p, a, st));
+    return e == cudaSuccess ? VC_OK : VC_ERR_CUDA;
+}
+
+}  // extern "C"

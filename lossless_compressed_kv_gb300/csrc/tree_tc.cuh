@@ -138,8 +138,8 @@ struct Cfg {
 };
 
 // Blocks of a request's context: 0 for one that is refused.
-template <int BK>
-__device__ inline int blocks_of(const Args &a, int b) {
+template <int BK, class A>
+__device__ inline int blocks_of(const A &a, int b) {
     const int len = a.lens[b];
     return len >= a.n_q && len <= a.max_len ? ceil_div(len, BK) : 0;
 }
@@ -159,8 +159,8 @@ struct Deal {
 
 // Blocks (of one kv head) of all requests and of those before request
 // `until`: every warp adds them up for itself, a lane per request.
-template <int BK>
-__device__ inline void sum_blocks(const Args &a, int until, int lane, int &total, int &before) {
+template <int BK, class A>
+__device__ inline void sum_blocks(const A &a, int until, int lane, int &total, int &before) {
     total = before = 0;
     for (int b = lane; b < a.batch; b += 32) {
         const int n = blocks_of<BK>(a, b);
@@ -175,8 +175,8 @@ __device__ inline void sum_blocks(const Args &a, int until, int lane, int &total
 
 // The request that holds block f of the blocks laid end to end, and the block's
 // place among that request's (all kv heads); by a warp.
-template <int BK>
-__device__ inline void find_block(const Args &a, int f, int lane, int &b, int &rest) {
+template <int BK, class A>
+__device__ inline void find_block(const A &a, int f, int lane, int &b, int &rest) {
     int before = 0;
     for (int b0 = 0;; b0 += 32) {
         const int n = b0 + lane < a.batch ? blocks_of<BK>(a, b0 + lane) * a.hkv : 0;
@@ -206,7 +206,8 @@ struct Walk {
     int seg_b, seg_kvh, seg_len, seg_blk, seg_n;
     bool whole, at_start;
 
-    __device__ void begin(const Args &a, int b_, int rest, int left_) {
+    template <class A>
+    __device__ void begin(const A &a, int b_, int rest, int left_) {
         b = b_;
         left = left_;
         first = true;
@@ -218,7 +219,8 @@ struct Walk {
         }
     }
     // The next segment.
-    __device__ bool next(const Args &a) {
+    template <class A>
+    __device__ bool next(const A &a) {
         if (left <= 0) return false;
         while (blk >= nblk) {  // the next unit that has blocks
             blk = 0;
