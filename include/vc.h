@@ -819,6 +819,117 @@ VC_API vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, co
                              vc_stream_t stream);
 
 /*
+ * Pages of a pool, and who holds them.  The tables that the attention calls
+ * read are made and kept here: a row (request) holds pages, requests may
+ * share them, a shared page is replaced before it is written to, and pages go
+ * back.  Page ids are those of every layer's pools alike (and of an 8-bit
+ * cache's), so one map serves a model.
+ *  table    device int32 [batch][max_blocks]: the block table
+ *  blocks   device int32 [batch]: pages that each row holds, its first
+ *           entries; what lies behind them is not read
+ *  refs     device int32 [num_pages]: rows that hold the page (the caller may
+ *           add references of its own); 0: free.  All 0, with blocks 0, is a
+ *           pool at the start.
+ * Calls on one map follow one another on a stream.  Ids that are handed out
+ * follow from the state alone: the lowest free ones, rows in order.
+ * num_pages < 2^31 - 1.  A page id out of range, or one that refs says
+ * nobody holds, is reported (VC_ERR_BAD_INDEX in dev_status).
+ */
+typedef struct {
+    int32_t *table;
+    int32_t *blocks;
+    int32_t *refs;
+    int64_t num_pages;
+    int32_t batch;
+    int32_t max_blocks;
+} vc_page_map;
+
+/* Bytes that vc_pages_reserve and vc_pages_compact need (4-byte aligned; calls
+ * that may run at the same time take one each). */
+VC_API size_t vc_pages_workspace_bytes(const vc_page_map *map);
+
+/*
+ * vc_pages_free -- row b gives back the pages behind those that keep[b] tokens
+ * take (0: all of them, -1 and below: none): their references are one fewer,
+ * their entries -1.
+ *  keep  device int32 [batch]
+ */
+VC_API vc_status vc_pages_free(const vc_page_map *map, const int32_t *keep, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_pages_fork -- row dst[i] becomes a copy of row src[i] that shares its
+ * pages: the ones that seq_lens[src[i]] tokens take, the last of them in part
+ * (vc_pages_reserve gives the fork one of its own before it is written to).
+ *  seq_lens  device int32 [batch]; seq_lens[dst[i]] is set
+ *  src, dst  device int32 [n]: rows; -1 beside -1 is no pair.  A row may be
+ *            the source of many.
+ * A pair whose row is out of range, whose target holds pages, is named as a
+ * target twice or is a source as well, or whose source holds too few pages is
+ * left out and reported (VC_ERR_BAD_INDEX).
+ */
+VC_API vc_status vc_pages_fork(const vc_page_map *map, int32_t *seq_lens, const int32_t *src, const int32_t *dst,
+                               int32_t n, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_pages_reserve -- make room for positions seq_lens[b] .. want[b] - 1 of
+ * each row, in pages that no other row holds.  Rows are served in order:
+ * held pages of those positions that are shared are replaced by free ones
+ * (but where all rows that hold a page write to it in this call, the last of
+ * them keeps it), then the row is lengthened.
+ *  seq_lens  device int32 [batch]: tokens that each row holds
+ *  want      device int32 [batch]; not above seq_lens[b]: nothing is asked
+ *  granted   device int32 [batch]: 1, or 0 for a row that did not get its
+ *            pages.  From the first row on that does not find all of its
+ *            pages free, rows that ask for any get none and stay as they
+ *            were (so do those behind that would need none).
+ *  copy_src, copy_dst  device int32 [batch]: the page with tokens that row b
+ *            gave up and the one it got for it, as vc_pages_copy takes them
+ *            (on this stream, before the row is written to); -1 where there
+ *            is none
+ * A row of impossible lengths (negative, more tokens than its pages hold, more
+ * than max_blocks) or bad pages is left as it was, not granted and reported
+ * (VC_ERR_BAD_INDEX).  seq_lens is not changed.
+ */
+VC_API vc_status vc_pages_reserve(const vc_page_map *map, const int32_t *seq_lens, const int32_t *want,
+                                  int32_t *granted, int32_t *copy_src, int32_t *copy_dst, void *workspace,
+                                  size_t workspace_bytes, int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_pages_compact -- move a pool's N live pages (refs > 0) to ids below N,
+ * with as few moves as that takes: the k-th free id below N gets the k-th
+ * live page from N on.  table and refs are rewritten; the pages' content
+ * follows by vc_pages_copy with move_src, move_dst and moves, on this stream,
+ * before anything reads the pools.
+ *  move_src, move_dst  device int32 [max_moves], max_moves >= num_pages / 2:
+ *                      the moves in order, -1 behind them
+ *  moves               device int32 [1]: how many
+ *  remap               device int32 [num_pages]: each live page's new id (for
+ *                      references that the caller keeps elsewhere), -1 for a
+ *                      free one
+ */
+VC_API vc_status vc_pages_compact(const vc_page_map *map, int32_t *move_src, int32_t *move_dst, int32_t max_moves,
+                                  int32_t *moves, int32_t *remap, void *workspace, size_t workspace_bytes,
+                                  int32_t *dev_status, vc_stream_t stream);
+
+/*
+ * vc_pages_copy -- copy whole pages within each of several arrays: pools of K
+ * or V in any format, scales of an 8-bit cache, anything with a fixed number of
+ * bytes a page.
+ *  arrays    host array of n_arrays: page p of array i at data + p *
+ *            page_bytes; both multiples of 4 (of 16: faster)
+ *  src, dst  device int32 [n]: pages; -1 beside -1 is no copy.  No page is the
+ *            target of two copies, or of one and the source of another.
+ *  count     device int32 [1] or NULL: only the first *count
+ */
+typedef struct {
+    void *data;
+    int64_t page_bytes;
+} vc_page_array;
+VC_API vc_status vc_pages_copy(const vc_page_array *arrays, int32_t n_arrays, int64_t num_pages, const int32_t *src,
+                               const int32_t *dst, int32_t n, const int32_t *count, int32_t *dev_status,
+                               vc_stream_t stream);
+
+/*
  * vc_debug_set_wait_fault -- fault injection for tests of the bounded device
  * waits (host-side switch, process-wide, off by default; not for production
  * use).  Every wait of a kernel on a copy or on another warp gives up after

@@ -57,6 +57,15 @@ class PagedKV8Struct(C.Structure):
                 ("max_blocks", C.c_int32), ("num_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("code", C.c_int32)]
 
 
+class PageMapStruct(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("blocks", C.c_void_p), ("refs", C.c_void_p), ("num_pages", C.c_int64),
+                ("batch", C.c_int32), ("max_blocks", C.c_int32)]
+
+
+class PageArrayStruct(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_bytes", C.c_int64)]
+
+
 class RotaryStruct(C.Structure):
     _fields_ = [("theta", C.c_float), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("factor", C.c_float),
                 ("original_len", C.c_int32), ("low_turns", C.c_float), ("high_turns", C.c_float),
@@ -126,6 +135,12 @@ _SIG = {
     "vc_kv8_workspace_bytes": (C.c_size_t, [C.POINTER(PagedKV8Struct), C.c_int32, C.c_int32, C.c_int32]),
     "vc_kv8_attn": (C.c_int, [_P, C.c_int32, C.c_int32, C.POINTER(PagedKV8Struct), _P, C.c_float, _P, C.c_int32,
                               C.c_int32, _P, C.c_size_t, _P, _P]),
+    "vc_pages_workspace_bytes": (C.c_size_t, [C.POINTER(PageMapStruct)]),
+    "vc_pages_free": (C.c_int, [C.POINTER(PageMapStruct), _P, _P, _P]),
+    "vc_pages_fork": (C.c_int, [C.POINTER(PageMapStruct), _P, _P, _P, C.c_int32, _P, _P]),
+    "vc_pages_reserve": (C.c_int, [C.POINTER(PageMapStruct), _P, _P, _P, _P, _P, _P, C.c_size_t, _P, _P]),
+    "vc_pages_compact": (C.c_int, [C.POINTER(PageMapStruct), _P, _P, C.c_int32, _P, _P, _P, C.c_size_t, _P, _P]),
+    "vc_pages_copy": (C.c_int, [C.POINTER(PageArrayStruct), C.c_int32, C.c_int64, _P, _P, C.c_int32, _P, _P, _P]),
     "vc_draft_attn_static": (C.c_int, [_P, C.c_int32, C.POINTER(PagedKVStruct), C.c_float, _P, C.c_int32, _P, _P]),
     "vc_static_scratch_bytes": (C.c_size_t, []),
     "vc_stagger_plan": (C.c_int, [_P, C.c_int32, C.c_int32, _P, _P]),
@@ -798,6 +813,124 @@ def kv8_attn(q, kv8: PagedKV8, softmax_scale: float, out, max_seq_len: int, work
         None if mask is None else _need("mask", mask, _I64, (b, n_q), dev), softmax_scale,
         _need("out", out, out.dtype, shape, dev), _DTYPES.get(out.dtype, -1), max_seq_len, *_room(workspace, dev),
         _status(status, dev), _on(stream, dev)), "vc_kv8_attn")
+
+
+# ---------------------------------------------------------------------------
+# pages of a pool
+# ---------------------------------------------------------------------------
+
+_PAGE_MAP = struct.Struct("PPPqii").pack   # PageMapStruct
+
+
+@dataclass
+class PageMap:
+    """Which row holds which pages (vc_page_map in include/vc.h): block table
+    int32 [batch, max_blocks], pages that each row holds int32 [batch],
+    references of each page int32 [num_pages]."""
+    table: torch.Tensor
+    blocks: torch.Tensor
+    refs: torch.Tensor
+
+    @staticmethod
+    def allocate(num_pages: int, batch: int, max_blocks: int, device="cuda") -> "PageMap":
+        """A map of a pool nobody holds a page of."""
+        return PageMap(torch.full((batch, max_blocks), -1, dtype=torch.int32, device=device),
+                       torch.zeros(batch, dtype=torch.int32, device=device),
+                       torch.zeros(num_pages, dtype=torch.int32, device=device))
+
+
+def _map(m: PageMap, dev: int) -> PageMapStruct:
+    b, w = m.table.shape
+    n = m.refs.shape
+    return PageMapStruct.from_buffer_copy(_PAGE_MAP(
+        _need("table", m.table, _I32, (b, w), dev), _need("blocks", m.blocks, _I32, (b,), dev),
+        _need("refs", m.refs, _I32, n, dev), n[0], b, w))
+
+
+class PageArrays:
+    """Tensors whose first axis is a pool's pages (K and V pools of any format,
+    scales), as vc_pages_copy takes them; built once, kept by the caller."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        n = {int(t.shape[0]) for t in self.tensors}
+        if len(n) > 1:
+            raise ValueError("all arrays hold the same pages")
+        self.num_pages = n.pop() if n else 0
+        self._read(_device())
+
+    def _read(self, dev):
+        for t in self.tensors:
+            if not t.is_contiguous():
+                raise ValueError("arrays of pages must be contiguous")
+        self.structs = (PageArrayStruct * len(self.tensors))(
+            *[PageArrayStruct(_here("array", t, dev), t.nbytes // max(1, self.num_pages)) for t in self.tensors])
+        self.device = dev
+
+    def _as_read(self) -> bool:
+        return all(t.data_ptr() == s.data for t, s in zip(self.tensors, self.structs))
+
+
+def pages_workspace_bytes(pages: PageMap) -> int:
+    b, w = pages.table.shape
+    return int(_lib.vc_pages_workspace_bytes(C.byref(PageMapStruct(
+        num_pages=int(pages.refs.shape[0]), batch=int(b), max_blocks=int(w)))))
+
+
+def pages_free(pages: PageMap, keep, status=None, stream=None):
+    """vc_pages_free: row b keeps the pages of keep[b] tokens (int32 [B]; -1:
+    all) and gives the others back."""
+    dev = _device()
+    ms = _map(pages, dev)
+    _check(_lib.vc_pages_free(C.byref(ms), _need("keep", keep, _I32, (ms.batch,), dev), _status(status, dev),
+                              _on(stream, dev)), "vc_pages_free")
+
+
+def pages_fork(pages: PageMap, seq_lens, src, dst, status=None, stream=None):
+    """vc_pages_fork: rows dst (int32 [n]) share the pages of rows src;
+    seq_lens int32 [B] follows."""
+    dev, shape = _device(), src.shape
+    ms = _map(pages, dev)
+    n, = shape
+    _check(_lib.vc_pages_fork(
+        C.byref(ms), _need("seq_lens", seq_lens, _I32, (ms.batch,), dev), _need("src", src, _I32, shape, dev),
+        _need("dst", dst, _I32, shape, dev), n, _status(status, dev), _on(stream, dev)), "vc_pages_fork")
+
+
+def pages_reserve(pages: PageMap, seq_lens, want, granted, copy_src, copy_dst, workspace, status=None, stream=None):
+    """vc_pages_reserve: room for want[b] tokens in pages of the row's own;
+    all int32 [B]; copy_src / copy_dst go to pages_copy."""
+    dev = _device()
+    ms = _map(pages, dev)
+    p = [_need(name, t, _I32, (ms.batch,), dev) for name, t in (
+        ("seq_lens", seq_lens), ("want", want), ("granted", granted), ("copy_src", copy_src), ("copy_dst", copy_dst))]
+    _check(_lib.vc_pages_reserve(C.byref(ms), *p, *_room(workspace, dev), _status(status, dev), _on(stream, dev)),
+           "vc_pages_reserve")
+
+
+def pages_compact(pages: PageMap, move_src, move_dst, moves, remap, workspace, status=None, stream=None):
+    """vc_pages_compact: live pages to the lowest ids; move_src / move_dst
+    int32 [num_pages // 2 or more], moves int32 [1], remap int32 [num_pages]."""
+    dev, shape = _device(), move_src.shape
+    ms = _map(pages, dev)
+    n, = shape
+    _check(_lib.vc_pages_compact(
+        C.byref(ms), _need("move_src", move_src, _I32, shape, dev), _need("move_dst", move_dst, _I32, shape, dev), n,
+        _need("moves", moves, _I32, (1,), dev), _need("remap", remap, _I32, (ms.num_pages,), dev),
+        *_room(workspace, dev), _status(status, dev), _on(stream, dev)), "vc_pages_compact")
+
+
+def pages_copy(arrays: PageArrays, src, dst, count=None, status=None, stream=None):
+    """vc_pages_copy: pages src (int32 [n]) to pages dst in every array; only
+    the first count[0] where count (int32 [1]) is given."""
+    dev, shape = _device(), src.shape
+    n, = shape
+    if arrays.device != dev or not arrays._as_read():
+        arrays._read(dev)
+    _check(_lib.vc_pages_copy(
+        arrays.structs, len(arrays.tensors), arrays.num_pages, _need("src", src, _I32, shape, dev),
+        _need("dst", dst, _I32, shape, dev), n, None if count is None else _need("count", count, _I32, (1,), dev),
+        _status(status, dev), _on(stream, dev)), "vc_pages_copy")
 
 
 # ---------------------------------------------------------------------------
