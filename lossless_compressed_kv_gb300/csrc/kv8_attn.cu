@@ -1,7 +1,7 @@
 // vc_kv8_attn: attention over a cache held in 8 bits (see kv8.cuh).
 #include <cmath>
 
-#include "kv8_few.cuh"
+#include "kv8_tc.cuh"
 
 namespace vc {
 bool encode_pool8(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d);
@@ -14,6 +14,14 @@ __global__ void __launch_bounds__(kv8::Few<D, NT>::THREADS, kv8::Few<D, NT>::CTA
     extern __shared__ __align__(1024) uint8_t smem[];
     kv8::few_warp<D, NT, E4M3>(a, smem);
     pdl_trigger();
+}
+
+template <int D, int QT, bool E4M3>
+__global__ void __launch_bounds__(kv8::Tc<D, QT>::THREADS, kv8::Tc<D, QT>::MIN_CTAS)
+    kv8_tc_kernel(const __grid_constant__ kv8::Args a) {
+    pdl_wait();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    kv8::tc_cta<D, QT, E4M3>(a, smem);
 }
 
 template <int D, int BK>
@@ -29,41 +37,73 @@ bool supported(const vc_paged_kv8 &kv, int n_q, int hq) {
            hq % hkv == 0 && hq / hkv <= VC_MAX_GQA_GROUP && n_q >= 1 && n_q <= VC_MAX_VERIFY_QUERIES;
 }
 
+// Rows that a warp of kv8_few.cuh holds at most.
+constexpr int kFewRows = 32;
+
 // How a call is laid out over the GPU.
 struct Plan {
-    int nt;                         // eights of rows of a warp
-    int lanes, lane_rows, groups;   // chunks of rows, their rows, ranges of the context
+    int nt, tiles;                  // kv8_few.cuh: eights of rows of a warp; else tiles of a CTA
+    int lanes, lane_rows, groups;   // CTAs that share a range, the rows of one, ranges of the context
     int64_t slots() const { return (int64_t)groups * lanes * 2 * lane_rows; }  // partial rows
 };
 Plan plan_of(const vc_paged_kv8 &kv, int n_q, int hq, int max_seq_len) {
     const int rows = n_q * (hq / kv.num_kv_heads);
-    Plan p;
-    p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    p.lane_rows = 8 * p.nt;
-    p.lanes = ceil_div(rows, p.lane_rows);
-    const int64_t pages = (int64_t)kv.batch * kv.num_kv_heads * ceil_div(max_seq_len, kPage);
-    const int most = tree::kSMs * 4 * (p.nt == 1 ? 4 : p.nt == 2 ? 3 : 2);
-    p.groups = (int)(pages < 1 ? 1 : pages < most ? pages : most);
+    Plan p{};
+    int most, block;
+    if (rows <= kFewRows) {
+        p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+        p.lanes = 1;
+        p.lane_rows = 8 * p.nt;
+        most = tree::kSMs * 4 * (p.nt == 1 ? 4 : p.nt == 2 ? 3 : 2);
+        block = kPage;
+    } else {
+        const int tiles = ceil_div(rows, kv8::kTileRows);
+        p.lanes = tiles == 4 ? 2 : 1;
+        p.tiles = tiles / p.lanes;
+        p.lane_rows = p.tiles * kv8::kTileRows;
+        most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / p.lanes;
+        block = kv8::Tc<128, 1>::BK;
+    }
+    const int64_t blocks = (int64_t)kv.batch * kv.num_kv_heads * ceil_div(max_seq_len, block);
+    p.groups = (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
     return p;
 }
 size_t workspace_of(const Plan &p, int d) { return (size_t)p.slots() * (d + 2) * sizeof(float); }
 
+template <int D, int BK>
+cudaError_t launch_join(const kv8::Args &a, int lane_rows, cudaStream_t st) {
+    // ranges that a unit spans, were the lengths alike: a warp reads eight at once
+    const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
+    const dim3 grid(a.batch * a.hkv, ceil_div(a.rows, kv8::kJoinWarps / W));
+    const cudaError_t e = launch_pdl(kv8_join_kernel<D, BK>, grid, kv8::kJoinWarps * 32, 0, st, a, W, lane_rows);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
 template <int D, int NT, bool E4M3>
 cudaError_t launch_few(const kv8::Args &a, cudaStream_t st) {
     using F = kv8::Few<D, NT>;
     cudaError_t e = set_smem_limit((const void *)kv8_few_kernel<D, NT, E4M3>, F::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kv8_few_kernel<D, NT, E4M3>, dim3(ceil_div(a.groups, F::WARPS), a.lanes), F::THREADS, F::SMEM, st, a);
+    e = launch_pdl(kv8_few_kernel<D, NT, E4M3>, ceil_div(a.groups, F::WARPS), F::THREADS, F::SMEM, st, a);
+    return e != cudaSuccess ? e : launch_join<D, kPage>(a, F::ROWS, st);
+}
+template <int D, int QT, bool E4M3>
+cudaError_t launch_tc(const kv8::Args &a, cudaStream_t st) {
+    using C = kv8::Tc<D, QT>;
+    // (the warps share out the registers that the block is launched with)
+    static const int regs = [] {
+        cudaFuncAttributes f;
+        return cudaFuncGetAttributes(&f, kv8_tc_kernel<D, QT, E4M3>) == cudaSuccess ? f.numRegs : 0;
+    }();
+    if (regs * C::WARPS < C::REGS_SOFTMAX * C::SM_WARPS + C::REGS_OTHER * 4) return cudaErrorInvalidConfiguration;
+    cudaError_t e = set_smem_limit((const void *)kv8_tc_kernel<D, QT, E4M3>, C::SMEM);
     if (e != cudaSuccess) return e;
-    // ranges that a unit spans, were the lengths alike: a warp reads eight at once
-    const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
-    const dim3 grid(a.batch * a.hkv, ceil_div(a.rows, kv8::kJoinWarps / W));
-    e = launch_pdl(kv8_join_kernel<D, kPage>, grid, kv8::kJoinWarps * 32, 0, st, a, W, F::ROWS);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    e = launch_pdl(kv8_tc_kernel<D, QT, E4M3>, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
+    return e != cudaSuccess ? e : launch_join<D, C::BK>(a, C::ROWS, st);
 }
 template <int D, bool E4M3>
 cudaError_t launch(const Plan &p, const kv8::Args &a, cudaStream_t st) {
-    return p.nt == 1 ? launch_few<D, 1, E4M3>(a, st) : p.nt == 2 ? launch_few<D, 2, E4M3>(a, st) : launch_few<D, 4, E4M3>(a, st);
+    if (p.nt) return p.nt == 1 ? launch_few<D, 1, E4M3>(a, st) : p.nt == 2 ? launch_few<D, 2, E4M3>(a, st) : launch_few<D, 4, E4M3>(a, st);
+    return p.tiles == 1 ? launch_tc<D, 1, E4M3>(a, st) : p.tiles == 2 ? launch_tc<D, 2, E4M3>(a, st) : launch_tc<D, 3, E4M3>(a, st);
 }
 
 }  // namespace

@@ -54,7 +54,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
     constexpr int KS = D / 16;       // steps of S, tiles of O
     constexpr int BK = kPage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int range = blockIdx.x * F::WARPS + warp, chunk = blockIdx.y;
+    const int range = blockIdx.x * F::WARPS + warp;
     uint8_t *ring = smem + warp * F::STAGES * F::STAGE;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + F::OFF_BAR) + warp * F::STAGES;
     float2 *scales = reinterpret_cast<float2 *>(smem + F::OFF_SC) + warp * F::STAGES;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
         float rf[NT][2], m[NT][2], l[NT][2], acc[NT][KS][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = chunk * F::ROWS + n * 8 + g;
+            const int r = n * 8 + g;
             uint32_t u[KS * 2];
             if (r < a.rows) {
                 const int64_t row = ((int64_t)w.seg_b * a.n_q + r / a.grp) * a.hq + w.seg_kvh * a.grp + r % a.grp;
@@ -219,7 +219,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int r = chunk * F::ROWS + n * 8 + 2 * t + c;
+                        const int r = n * 8 + 2 * t + c;
                         const unsigned long long seen =
                             r < a.rows ? tree::seen_bits(mask_of(a, w.seg_b, r / a.grp), key0, base) : 0ull;
                         if (!((seen >> g) & 1)) x[n][c] = -INFINITY;
@@ -315,7 +315,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                 ls += __shfl_xor_sync(0xffffffffu, ls, 4);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
-                const int lr = n * 8 + 2 * t + c, r = chunk * F::ROWS + lr;
+                const int r = n * 8 + 2 * t + c;
                 if (r >= a.rows) continue;
                 // a row that is left out or saw no key: zeros (m = -infinity); one
                 // that met a NaN: NaN (m = +infinity, which no other range outweighs);
@@ -324,7 +324,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                 const bool zero = !alive || mask_of(a, w.seg_b, r / a.grp) == 0 || (m[n][c] == -INFINITY && ls == 0.0f);
                 const float f = zero ? 0.0f : vref / ls;
                 const int64_t orow = ((int64_t)w.seg_b * a.n_q + r / a.grp) * a.hq + w.seg_kvh * a.grp + r % a.grp;
-                const int64_t prow = (((int64_t)range * a.lanes + chunk) * 2 + !w.at_start) * F::ROWS + lr;
+                const int64_t prow = ((int64_t)range * 2 + !w.at_start) * F::ROWS + r;
                 float o[D / 8];
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
