@@ -23,8 +23,8 @@ namespace vc {
 namespace kv8 {
 
 struct Args {
-    CUtensorMap kmap, vmap;
-    const float *ks, *vs;  // [pages][kv heads]
+    const uint8_t *kc, *vc;  // codes [pages][kv heads][16][D]
+    const float *ks, *vs;    // [pages][kv heads]
     const uint16_t *q;     // [B][n_q][Hq][D]
     int64_t n_pages;
     const int32_t *table, *lens;

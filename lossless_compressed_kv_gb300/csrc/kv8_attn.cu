@@ -1,10 +1,9 @@
 // vc_kv8_attn: attention over a cache held in 8 bits (see kv8.cuh).
 #include <cmath>
 
-#include "kv8_tc.cuh"
+#include "kv8_one.cuh"
 
 namespace vc {
-bool encode_pool8(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d);
 namespace {
 
 template <int D, int NT, bool E4M3>
@@ -16,9 +15,15 @@ __global__ void __launch_bounds__(kv8::Few<D, NT>::THREADS, kv8::Few<D, NT>::CTA
     pdl_trigger();
 }
 
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kv8::One<D>::THREADS, 1) kv8_one_kernel(const __grid_constant__ kv8::Args a) {
+    pdl_wait();
+    extern __shared__ __align__(1024) uint8_t smem[];
+    kv8::one_cta<D, E4M3>(a, smem);
+}
+
 template <int D, int QT, bool E4M3>
-__global__ void __launch_bounds__(kv8::Tc<D, QT>::THREADS, kv8::Tc<D, QT>::MIN_CTAS)
-    kv8_tc_kernel(const __grid_constant__ kv8::Args a) {
+__global__ void __launch_bounds__(kv8::Tc<D, QT>::THREADS, 1) kv8_tc_kernel(const __grid_constant__ kv8::Args a) {
     pdl_wait();
     extern __shared__ __align__(1024) uint8_t smem[];
     kv8::tc_cta<D, QT, E4M3>(a, smem);
@@ -61,8 +66,8 @@ Plan plan_of(const vc_paged_kv8 &kv, int n_q, int hq, int max_seq_len) {
         p.lanes = tiles == 4 ? 2 : 1;
         p.tiles = tiles / p.lanes;
         p.lane_rows = p.tiles * kv8::kTileRows;
-        most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / p.lanes;
-        block = kv8::Tc<128, 1>::BK;
+        most = tree::kSMs / p.lanes;
+        block = kv8::One<128>::BK;
     }
     const int64_t blocks = (int64_t)kv.batch * kv.num_kv_heads * ceil_div(max_seq_len, block);
     p.groups = (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
@@ -86,24 +91,27 @@ cudaError_t launch_few(const kv8::Args &a, cudaStream_t st) {
     e = launch_pdl(kv8_few_kernel<D, NT, E4M3>, ceil_div(a.groups, F::WARPS), F::THREADS, F::SMEM, st, a);
     return e != cudaSuccess ? e : launch_join<D, kPage>(a, F::ROWS, st);
 }
-template <int D, int QT, bool E4M3>
-cudaError_t launch_tc(const kv8::Args &a, cudaStream_t st) {
-    using C = kv8::Tc<D, QT>;
-    // (the warps share out the registers that the block is launched with)
+// (C: One or Tc)
+template <class C, int D, void (*kernel)(kv8::Args)>
+cudaError_t launch_tiles(const kv8::Args &a, cudaStream_t st) {
+    // the warps share out the registers that the block is launched with
     static const int regs = [] {
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, kv8_tc_kernel<D, QT, E4M3>) == cudaSuccess ? f.numRegs : 0;
+        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
     }();
-    if (regs * C::WARPS < C::REGS_SOFTMAX * C::SM_WARPS + C::REGS_OTHER * 4) return cudaErrorInvalidConfiguration;
-    cudaError_t e = set_smem_limit((const void *)kv8_tc_kernel<D, QT, E4M3>, C::SMEM);
+    if (regs * C::WARPS < C::REGS_SOFTMAX * C::SM_WARPS + C::REGS_OTHER * (C::WARPS - C::SM_WARPS))
+        return cudaErrorInvalidConfiguration;
+    cudaError_t e = set_smem_limit((const void *)kernel, C::SMEM);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kv8_tc_kernel<D, QT, E4M3>, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
+    e = launch_pdl(kernel, a.groups * a.lanes, C::THREADS, C::SMEM, st, a);
     return e != cudaSuccess ? e : launch_join<D, C::BK>(a, C::ROWS, st);
 }
 template <int D, bool E4M3>
 cudaError_t launch(const Plan &p, const kv8::Args &a, cudaStream_t st) {
     if (p.nt) return p.nt == 1 ? launch_few<D, 1, E4M3>(a, st) : p.nt == 2 ? launch_few<D, 2, E4M3>(a, st) : launch_few<D, 4, E4M3>(a, st);
-    return p.tiles == 1 ? launch_tc<D, 1, E4M3>(a, st) : p.tiles == 2 ? launch_tc<D, 2, E4M3>(a, st) : launch_tc<D, 3, E4M3>(a, st);
+    return p.tiles == 1   ? launch_tiles<kv8::One<D>, D, kv8_one_kernel<D, E4M3>>(a, st)
+           : p.tiles == 2 ? launch_tiles<kv8::Tc<D, 2>, D, kv8_tc_kernel<D, 2, E4M3>>(a, st)
+                          : launch_tiles<kv8::Tc<D, 3>, D, kv8_tc_kernel<D, 3, E4M3>>(a, st);
 }
 
 }  // namespace
@@ -137,11 +145,9 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     const float scale_log2 = softmax_scale * 1.4426950408889634f;
     if (!supported(*kv, n_q, num_q_heads) || (out_dtype != VC_F32 && out_dtype != VC_BF16) || !std::isfinite(scale_log2))
         return VC_ERR_UNSUPPORTED;
-    // (the kernels count pages, and the rows of a pool, in 32 bits)
+    // (the kernels count the pages of a call in 32 bits)
     const int64_t held = (int64_t)kv->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
-    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX ||
-        kv->num_pages > INT32_MAX / kPage / kv->num_kv_heads)
-        return VC_ERR_UNSUPPORTED;
+    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX || kv->num_pages > INT32_MAX) return VC_ERR_UNSUPPORTED;
     if (kv->batch == 0) return VC_OK;
     if (!q || !out || !kv8_ok(kv) || !kv->seq_lens || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 31))
         return VC_ERR_INVALID_ARG;
@@ -149,6 +155,8 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     const int d = kv->head_dim;
     if (!workspace || workspace_bytes < workspace_of(p, d)) return VC_ERR_WORKSPACE;
     kv8::Args a;
+    a.kc = (const uint8_t *)kv->k_codes;
+    a.vc = (const uint8_t *)kv->v_codes;
     a.ks = kv->k_scales;
     a.vs = kv->v_scales;
     a.q = (const uint16_t *)q;
@@ -174,9 +182,6 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     a.status = dev_status;
     a.wait_ns = wait_fault().wait_ns;
     a.skip_copies = wait_fault().skip_copies;
-    if (!encode_pool8(&a.kmap, kv->k_codes, kv->num_pages, a.hkv, d) ||
-        !encode_pool8(&a.vmap, kv->v_codes, kv->num_pages, a.hkv, d))
-        return VC_ERR_CUDA;
     const cudaStream_t st = (cudaStream_t)stream;
     const bool e4m3 = kv->code == VC_E4M3;
     const cudaError_t e = d == 64 ? (e4m3 ? launch<64, true>(p, a, st) : launch<64, false>(p, a, st))

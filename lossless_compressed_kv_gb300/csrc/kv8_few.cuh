@@ -3,9 +3,11 @@
 // the cache's bytes bound.
 //
 // Every warp walks a range of its own, page by page, through a ring of pages
-// that it fills by TMA (a head block of K and one of V a page, rows swizzled):
-// no barrier joins warps, so their loads, products and exponentials overlap
-// freely.  Per page, on mma.sync with 16 keys or channels as M:
+// that it fills itself by asynchronous copies of 16 bytes a lane: no barrier
+// joins warps, so their loads, products and exponentials overlap freely.  (By
+// TMA, a head block of a page a copy, 8 x 32768 keys took 98 us, and 60 with
+// head_dim 64: the SM's TMA unit takes such small copies too slowly.)
+// Per page, on mma.sync with 16 keys or channels as M:
 //   S^T = K Q^T      16 keys x 8 rows, D / 16 steps
 //   O^T += V^T P^T   D / 16 tiles of 16 channels x 8 rows
 // With few rows the 128-row instructions of tcgen05 would spend their time on
@@ -31,11 +33,10 @@ struct Few {
     static constexpr int CTAS = NT == 1 ? 4 : NT == 2 ? 3 : 2;  // an SM holds
     static constexpr int TILE = kPage * D;          // a head block of codes
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int ROOM = (228 * 1024 / CTAS - 1024) / WARPS / (STAGE + 16);
+    static constexpr int ROOM = (228 * 1024 / CTAS - 1024) / WARPS / (STAGE + 8);
     static constexpr int STAGES = ROOM < 8 ? ROOM : 8;
     static_assert(STAGES >= 3, "ring depth");
-    static constexpr int OFF_BAR = WARPS * STAGES * STAGE;
-    static constexpr int OFF_SC = OFF_BAR + WARPS * STAGES * 8;
+    static constexpr int OFF_SC = WARPS * STAGES * STAGE;
     static constexpr int SMEM = OFF_SC + WARPS * STAGES * 8;
     static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the CTAs an SM holds");
     static constexpr int ROWS = 8 * NT;
@@ -56,14 +57,8 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int range = blockIdx.x * F::WARPS + warp;
     uint8_t *ring = smem + warp * F::STAGES * F::STAGE;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + F::OFF_BAR) + warp * F::STAGES;
     float2 *scales = reinterpret_cast<float2 *>(smem + F::OFF_SC) + warp * F::STAGES;
     if (range >= a.groups) return;
-    if (lane == 0) {
-        for (int i = 0; i < F::STAGES; ++i) mbar_init(&full[i], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
     int total, before, b0 = 0, rest = 0;
     tree::sum_blocks<BK>(a, 0, lane, total, before);
     const tree::Deal deal(total * a.hkv, a.groups);
@@ -74,9 +69,8 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
     // ---- the copies, STAGES pages ahead ----
     tree::Walk<BK> iw;
     iw.begin(a, b0, rest, mine);
-    uint32_t issued = 0, used = 0;
+    int fill = 0, use = 0;  // stages next filled and used
     int ii = 0, in = 0;  // place in the segment whose pages are being issued
-    const bool skips = block_skips(a.skip_copies);
     // ids and scales of 32 pages, a lane each; the ids are read a batch ahead
     int id_next = 0, id = 0;
     float ks = 0.0f, vs = 0.0f;
@@ -92,38 +86,40 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
         }
         return p;
     };
+    // (a group of copies each time, so that what is under way is counted in pages)
     auto issue = [&]() {
-        if (ii == in) {
-            if (!iw.next(a)) return;
-            ii = 0;
-            in = iw.seg_n;
-            id_next = load_ids(0);
+        if (ii < in || iw.next(a)) {
+            if (ii == in) {
+                ii = 0;
+                in = iw.seg_n;
+                id_next = load_ids(0);
+            }
+            if (ii % 32 == 0) {
+                id = id_next;
+                const int64_t at = (int64_t)id * a.hkv + iw.seg_kvh;
+                ks = a.ks[at];
+                vs = a.vs[at];
+                id_next = load_ids(ii + 32);
+            }
+            const int p = __shfl_sync(0xffffffffu, id, ii % 32);
+            const float pk = __shfl_sync(0xffffffffu, ks, ii % 32), pv = __shfl_sync(0xffffffffu, vs, ii % 32);
+            ++ii;
+            if (lane == 0) scales[fill] = make_float2(scale_of(pk), scale_of(pv));
+            const int64_t from = ((int64_t)p * a.hkv + iw.seg_kvh) * F::TILE;
+            uint8_t *to = ring + fill * F::STAGE;
+#pragma unroll
+            for (int e = lane; e < F::TILE / 16; e += 32) {
+                const int off = piece_at<D>(e / (D / 16), e % (D / 16));
+                cp_async16(to + off, a.kc + from + e * 16);
+                cp_async16(to + F::TILE + off, a.vc + from + e * 16);
+            }
+            if (++fill == F::STAGES) fill = 0;
         }
-        if (ii % 32 == 0) {
-            id = id_next;
-            const int64_t at = (int64_t)id * a.hkv + iw.seg_kvh;
-            ks = a.ks[at];
-            vs = a.vs[at];
-            id_next = load_ids(ii + 32);
-        }
-        const int p = __shfl_sync(0xffffffffu, id, ii % 32);
-        const float pk = __shfl_sync(0xffffffffu, ks, ii % 32), pv = __shfl_sync(0xffffffffu, vs, ii % 32);
-        ++ii;
-        if (skips) return;
-        const int s = issued % F::STAGES;
-        if (lane == 0) {
-            scales[s] = make_float2(scale_of(pk), scale_of(pv));
-            mbar_arrive_expect_tx(&full[s], F::STAGE);
-            const int y = (p * a.hkv + iw.seg_kvh) * kPage;
-            vtc::tma2d(ring + s * F::STAGE, &a.kmap, 0, y, &full[s]);
-            vtc::tma2d(ring + s * F::STAGE + F::TILE, &a.vmap, 0, y, &full[s]);
-        }
-        ++issued;
+        cp_async_commit();
     };
 #pragma unroll 1
     for (int i = 0; i < F::STAGES; ++i) issue();
 
-    bool alive = true;
     tree::Walk<BK> w;
     w.begin(a, b0, rest, mine);
     while (w.next(a)) {
@@ -168,12 +164,12 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
         }
         float vref = 0.0f, inv_vref = 0.0f;
 #pragma unroll 1
-        for (int i = 0; i < w.seg_n && alive; ++i, ++used) {
-            const int s = used % F::STAGES;
-            alive = __all_sync(0xffffffffu, mbar_wait(&full[s], (used / F::STAGES) & 1, a.status, a.wait_ns));
-            if (!alive) break;
-            uint8_t *kt = ring + s * F::STAGE, *vt = kt + F::TILE;
-            const float2 sc2 = scales[s];
+        for (int i = 0; i < w.seg_n; ++i) {
+            cp_async_wait<F::STAGES - 1>();
+            __syncwarp();
+            uint8_t *kt = ring + use * F::STAGE, *vt = kt + F::TILE;
+            const float2 sc2 = scales[use];
+            if (++use == F::STAGES) use = 0;
             const int key0 = (w.seg_blk + i) * BK;
             // rows of V behind the request's end: whatever they hold, 0 times it is to be 0
             const bool ends = key0 + BK > w.seg_len;
@@ -302,7 +298,6 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                     }
                 }
             }
-            if (ends) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             issue();
         }
@@ -318,10 +313,8 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                 const int r = n * 8 + 2 * t + c;
                 if (r >= a.rows) continue;
                 // a row that is left out or saw no key: zeros (m = -infinity); one
-                // that met a NaN: NaN (m = +infinity, which no other range outweighs);
-                // one whose keys did not all come in time: zeros, and l = -1, which
-                // makes zeros of what it is joined with
-                const bool zero = !alive || mask_of(a, w.seg_b, r / a.grp) == 0 || (m[n][c] == -INFINITY && ls == 0.0f);
+                // that met a NaN: NaN (m = +infinity, which no other range outweighs)
+                const bool zero = mask_of(a, w.seg_b, r / a.grp) == 0 || (m[n][c] == -INFINITY && ls == 0.0f);
                 const float f = zero ? 0.0f : vref / ls;
                 const int64_t orow = ((int64_t)w.seg_b * a.n_q + r / a.grp) * a.hq + w.seg_kvh * a.grp + r % a.grp;
                 const int64_t prow = ((int64_t)range * 2 + !w.at_start) * F::ROWS + r;
@@ -344,13 +337,11 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                 }
                 if (!w.whole && g == 0) {
                     a.ws_ml[prow * 2] = zero ? -INFINITY : ls != ls ? INFINITY : m[n][c];
-                    a.ws_ml[prow * 2 + 1] = !alive ? -1.0f : zero ? 0.0f : ls;
+                    a.ws_ml[prow * 2 + 1] = zero ? 0.0f : ls;
                 }
             }
     }
-    // no copy may be under way when the CTA ends
-    for (; used < issued; ++used)
-        if (!mbar_wait(&full[used % F::STAGES], (used / F::STAGES) & 1, a.status, kWaitNs)) break;
+    cp_async_wait<0>();
 }
 
 }  // namespace kv8

@@ -245,6 +245,21 @@ def test_many_requests_and_long_ranges():
     check(out, h, qn, 0.125)
 
 
+@pytest.mark.parametrize("hq,n_q,d,code", [(32, 3, 64, "e4m3"), (64, 2, 128, "int8"), (8, 33, 128, "e4m3"), (8, 48, 64, "int8"),
+                                           (16, 64, 128, "int8"), (32, 40, 64, "e4m3"), (40, 64, 128, "e4m3"),
+                                           (64, 64, 64, "int8")])
+def test_long_ranges_of_many_rows(hq, n_q, d, code):
+    """Ranges of several units, and of more blocks than any ring holds."""
+    rng = np.random.default_rng(16)
+    lens = [12000, 6001, n_q, 70, 300, 9999, 4096, 150, 64, 2500]
+    c8, h = cache(rng, lens, 8, d, code)
+    qn, q = q_of(rng, (len(lens), n_q, hq, d))
+    out, st = run(q, c8, 1 / math.sqrt(d), max(lens))
+    assert st == 0
+    keep = [0, 2, 3, 7, 8] if n_q < 64 else [1, 2, 4]
+    check(out[keep], {**h, "lens": [lens[b] for b in keep], "table": h["table"][keep]}, qn[keep], 1 / math.sqrt(d))
+
+
 def odd_scales(s):
     s[::3] = 0.0
     s[1::7] = np.nan
@@ -301,8 +316,9 @@ def test_refused_and_idle_requests(n_q):
     check(out, h, qn, 0.125, only=[0, 2])
 
 
-@pytest.mark.parametrize("n_q", [1, 5, 40])
+@pytest.mark.parametrize("n_q", [12, 40])
 def test_waits_that_run_out(n_q):
+    """(Few rows are served without waits on other warps.)"""
     m, rng = vc(), np.random.default_rng(13)
     c8, h = cache(rng, [3000, 40], 2, 128, "int8")
     qn, q = q_of(rng, (2, n_q, 8, 128))
