@@ -24,6 +24,7 @@ namespace kv8 {
 
 struct Args {
     const uint8_t *kc, *vc;  // codes [pages][kv heads][16][D]
+    CUtensorMap kmap, vmap;  // the same for the TMA unit, a head block of a page a box (more than 128 rows)
     const float *ks, *vs;    // [pages][kv heads]
     const uint16_t *q;     // [B][n_q][Hq][D]
     int64_t n_pages;

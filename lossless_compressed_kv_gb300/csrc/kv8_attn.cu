@@ -4,6 +4,7 @@
 #include "kv8_one.cuh"
 
 namespace vc {
+bool encode_pool8(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d);
 namespace {
 
 template <int D, int NT, bool E4M3>
@@ -42,8 +43,11 @@ bool supported(const vc_paged_kv8 &kv, int n_q, int hq) {
            hq % hkv == 0 && hq / hkv <= VC_MAX_GQA_GROUP && n_q >= 1 && n_q <= VC_MAX_VERIFY_QUERIES;
 }
 
-// Rows that a warp of kv8_few.cuh holds at most.
-constexpr int kFewRows = 32;
+// Rows that go to kv8_few.cuh at most.  More go to kv8_one.cuh, whose time
+// hardly depends on their number (8 x 32768 keys, head_dim 128: 16 rows 112 us
+// in the first, 169 in the second; 20 rows 276 and 171: so many accumulators leave a scheduler
+// two warps.  head_dim 64: 32 rows 105 and 144 us).
+constexpr int few_rows(int d) { return d == 64 ? 32 : 16; }
 
 // How a call is laid out over the GPU.
 struct Plan {
@@ -55,7 +59,7 @@ Plan plan_of(const vc_paged_kv8 &kv, int n_q, int hq, int max_seq_len) {
     const int rows = n_q * (hq / kv.num_kv_heads);
     Plan p{};
     int most, block;
-    if (rows <= kFewRows) {
+    if (rows <= few_rows(kv.head_dim)) {
         p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
         p.lanes = 1;
         p.lane_rows = 8 * p.nt;
@@ -108,7 +112,10 @@ cudaError_t launch_tiles(const kv8::Args &a, cudaStream_t st) {
 }
 template <int D, bool E4M3>
 cudaError_t launch(const Plan &p, const kv8::Args &a, cudaStream_t st) {
-    if (p.nt) return p.nt == 1 ? launch_few<D, 1, E4M3>(a, st) : p.nt == 2 ? launch_few<D, 2, E4M3>(a, st) : launch_few<D, 4, E4M3>(a, st);
+    if (p.nt == 1) return launch_few<D, 1, E4M3>(a, st);
+    if (p.nt == 2) return launch_few<D, 2, E4M3>(a, st);
+    if constexpr (few_rows(D) > 16)
+        if (p.nt == 4) return launch_few<D, 4, E4M3>(a, st);
     return p.tiles == 1   ? launch_tiles<kv8::One<D>, D, kv8_one_kernel<D, E4M3>>(a, st)
            : p.tiles == 2 ? launch_tiles<kv8::Tc<D, 2>, D, kv8_tc_kernel<D, 2, E4M3>>(a, st)
                           : launch_tiles<kv8::Tc<D, 3>, D, kv8_tc_kernel<D, 3, E4M3>>(a, st);
@@ -145,9 +152,9 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     const float scale_log2 = softmax_scale * 1.4426950408889634f;
     if (!supported(*kv, n_q, num_q_heads) || (out_dtype != VC_F32 && out_dtype != VC_BF16) || !std::isfinite(scale_log2))
         return VC_ERR_UNSUPPORTED;
-    // (the kernels count the pages of a call in 32 bits)
+    // (the kernels count the pages of a call, and the rows of a pool, in 32 bits)
     const int64_t held = (int64_t)kv->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
-    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX || kv->num_pages > INT32_MAX) return VC_ERR_UNSUPPORTED;
+    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX || kv->num_pages > INT32_MAX / kPage / kv->num_kv_heads) return VC_ERR_UNSUPPORTED;
     if (kv->batch == 0) return VC_OK;
     if (!q || !out || !kv8_ok(kv) || !kv->seq_lens || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 31))
         return VC_ERR_INVALID_ARG;
@@ -182,6 +189,9 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     a.status = dev_status;
     a.wait_ns = wait_fault().wait_ns;
     a.skip_copies = wait_fault().skip_copies;
+    if (p.tiles > 1 && (!encode_pool8(&a.kmap, kv->k_codes, kv->num_pages, a.hkv, d) ||
+                        !encode_pool8(&a.vmap, kv->v_codes, kv->num_pages, a.hkv, d)))
+        return VC_ERR_CUDA;
     const cudaStream_t st = (cudaStream_t)stream;
     const bool e4m3 = kv->code == VC_E4M3;
     const cudaError_t e = d == 64 ? (e4m3 ? launch<64, true>(p, a, st) : launch<64, false>(p, a, st))

@@ -3,17 +3,18 @@
 // by parity and bounded waits) with codes instead of bf16 rows.
 //
 // tcgen05 takes both operands of one type, and whole numbers are not among
-// them: converter warps read codes and write fp16 into the ring that the
-// products read.  The conversion is exact, so Q and P in fp16 are all that is
-// rounded; e4m3 products of Q and P split in two would need as many
-// instructions and more softmax arithmetic, and not serve int8.  Shared memory
-// carries 64 KB written, and read by each tile, where HBM carries 32 (128 keys,
-// head_dim 128).
+// them: two warps turn blocks of codes (a ring filled by TMA) into fp16 in a
+// second ring, which the products read.  The conversion is exact, so Q and P
+// in fp16 are all that is rounded; e4m3 products of Q and P split in two would
+// need as many instructions and more softmax arithmetic, and not serve int8.
+// What it costs is shared memory: 32 KB of codes (128 keys, head_dim 128) are
+// written, read, written again as 64 KB and read by each tile.  At 128 bytes a
+// cycle that takes 1536 cycles for one tile, where HBM takes 1394.
 //
 // K's scales join the softmax scale, a factor a page; V's go with the
 // probabilities, relative to a reference (kv8.cuh) that moves like the running
-// maximum: rarely, with O rescaled.  The converters leave each block's
-// scales beside it.
+// maximum: rarely, with O rescaled.  The producer leaves each block's scales
+// beside its copies.
 #pragma once
 
 #include "kv8_few.cuh"
@@ -33,29 +34,29 @@ struct Tc {
     static_assert(NBUF <= 2 * QT, "phases that a parity tells apart");
     static constexpr int PG = BK / kPage;
     static constexpr int SLOT = BK * D * 2;   // a block in fp16
+    static constexpr int SLOT8 = BK * D;      // a block of codes
     static constexpr int QTILE = kTileRows * D * 2;
-    static constexpr int LAG = NBUF < QT ? 0 : 1;  // blocks that K is ahead of V
-    static constexpr int CONVERTERS = QT == 2 ? 7 : 3;
-    static constexpr int PAGES_AHEAD = QT == 2 ? 2 : 4, CODES = PAGES_AHEAD * kPage * D;  // each one's pages of codes under way
     static constexpr int OFF_KV = QT * QTILE;
     static constexpr int LIMIT = 226 * 1024;
-    static constexpr int FIT = (LIMIT - 4096 - OFF_KV - CONVERTERS * CODES) / SLOT;
-    static constexpr int SLOTS = FIT < 12 ? FIT : 12;
-    static_assert(SLOTS >= 3 && SLOTS / 2 + LAG + 3 <= kScaleRing, "ring depth");
-    static constexpr int OFF_CODES = OFF_KV + SLOTS * SLOT, OFF_SC = OFF_CODES + CONVERTERS * CODES;
+    static constexpr int SLOTS = D == 128 && QT < 3 ? 3 : 4;
+    static constexpr int FIT = (LIMIT - 2048 - OFF_KV - SLOTS * SLOT) / SLOT8;
+    static constexpr int SLOTS8 = FIT < 12 ? FIT : 12;
+    static_assert(SLOTS8 >= 4 && SLOTS8 / 2 + SLOTS / 2 + NBUF + 3 <= kScaleRing, "ring depths");
+    static constexpr int OFF_CODES = OFF_KV + SLOTS * SLOT;
+    static constexpr int OFF_SC = OFF_CODES + SLOTS8 * SLOT8;
     static constexpr int OFF_BAR = OFF_SC + kScaleRing * PG * 8;
     static constexpr int NS = NBUF < QT ? QT : NBUF;
-    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 1;
+    static constexpr int NBAR = 3 * QT + NS + NBUF + 2 * SLOTS + 2 * SLOTS8 + 1;
     static constexpr int SMEM = OFF_BAR + NBAR * 8 + 16;
     static_assert(SMEM <= LIMIT, "shared memory of the CTAs an SM holds");
     static constexpr int O_COL0 = NBUF * BK;
     static_assert(O_COL0 + QT * D <= 512, "TMEM columns");
     static constexpr int SM_WARPS = QT * 4;
-    // MMA issue and the converters give registers up for the softmax warps (2 x 128 x
-    // 184 + 2 x 128 x 72 = 512 x 128; 3 x 128 x 144 + 128 x 80 = 512 x 128)
-    static constexpr int WARPS = 16;
-    static constexpr int REGS_SOFTMAX = QT == 2 ? 184 : 144, REGS_OTHER = QT == 2 ? 72 : 80;
-    static_assert(SM_WARPS + 1 + CONVERTERS == WARPS, "roles");
+    // the last warpgroup: producer, MMA issue, two converters; it gives registers
+    // up for the softmax warps (2 x 128 x 216 + 128 x 72 <= 384 x 168; 3 x 128 x 136
+    // + 128 x 96 <= 512 x 128)
+    static constexpr int WARPS = 4 * QT + 4;
+    static constexpr int REGS_SOFTMAX = QT == 2 ? 216 : 136, REGS_OTHER = QT == 2 ? 72 : 96;
     static constexpr int THREADS = WARPS * 32;
     static constexpr int ROWS = QT * kTileRows;
 };
@@ -81,168 +82,6 @@ __device__ __forceinline__ void mul2(float &d0, float &d1, float b) {
         : "f"(b));
 }
 
-// The order of a range's blocks in the ring: within a segment V runs LAG
-// blocks behind K, as the products that read them do; they are done with in
-// this order as well.
-template <int BK, int LAG>
-struct Items {
-    tree::Walk<BK> w;
-    int i = 0, n = 0;   // step of the segment's n + LAG, and whether V is its next
-    bool v = true;
-    // the current item
-    int blk;
-    bool is_v;
-    __device__ bool next(const Args &a) {
-        for (;;) {
-            if (v) {  // the next step
-                v = false;
-                if (n == 0 || ++i == n + LAG) {
-                    if (!w.next(a)) {
-                        n = 0;
-                        v = true;
-                        return false;
-                    }
-                    i = 0;
-                    n = w.seg_n;
-                }
-                if (i < n) {
-                    blk = w.seg_blk + i;
-                    is_v = false;
-                    return true;
-                }
-            }
-            v = true;
-            if (i >= LAG) {
-                blk = w.seg_blk + i - LAG;
-                is_v = true;
-                return true;
-            }
-        }
-    }
-};
-
-// Converter warp `part` of C::CONVERTERS: every so many-th 64 keys from codes in
-// global memory to fp16 in the ring.  C::PAGES_AHEAD pages are under way by asynchronous
-// copies, each lane's pieces for itself alone.  (The SM's TMA unit takes copies
-// of a head block too slowly: 8 x 32768 keys 230 us; in registers they spill.)
-// The warps of a block of K leave the block's scales beside it.
-template <class C, int D, bool E4M3>
-__device__ __forceinline__ void convert(const Args &a, const tree::Walk<C::BK> &w, int part, uint8_t *skv, uint8_t *codes,
-                                        float2 *scales, uint64_t *full, uint64_t *empty) {
-    constexpr int BK = C::BK, IT = D / 64, U = 2 * IT;  // pieces of a page that a lane holds
-    constexpr int H = BK / 64, PG = 4, R = C::PAGES_AHEAD;  // parts of a block, pages of a part
-    static_assert(PG % R == 0 && BK % 64 == 0, "pages of a part");
-    const int lane = threadIdx.x & 31;
-    if (block_skips(a.skip_copies)) return;
-    Items<BK, C::LAG> it;
-    it.w = w;
-    int skip = part;
-    uint32_t seq = part, ahead = 0, ahead_k = 0;  // parts: this warp's, fetched; blocks of K so far
-    bool more = true;
-    struct Item {
-        bool there, is_v;
-        int rows;         // rows of V that hold tokens; below it nothing is kept
-        int id;           // lane p: page p
-        float2 sc;        // lane p: its scales (of a block of K)
-        uint32_t k;       // blocks of K before
-        int kvh;
-    };
-    auto fetch = [&]() {  // the next item of this warp
-        Item m;
-        for (int s = 0; s <= skip && more; ++s, ++ahead) {
-            if (ahead % H) continue;
-            more = it.next(a);
-            if (more && !it.is_v) ++ahead_k;
-        }
-        m.there = more;
-        m.k = ahead_k - 1;
-        const int half = (ahead - 1) % H;
-        skip = C::CONVERTERS - 1;
-        m.id = 0;
-        m.sc = make_float2(1.0f, 0.0f);
-        if (!m.there) return m;
-        m.is_v = it.is_v;
-        m.rows = m.is_v ? it.w.seg_len - it.blk * BK - half * 64 : BK;
-        m.kvh = it.w.seg_kvh;
-        const int pidx = (it.blk * H + half) * PG + lane;
-        // (pages behind the request's end: any valid page, masked and cleared)
-        if (lane < PG && pidx * kPage < it.w.seg_len) {
-            m.id = pidx < a.maxb ? a.table[(int64_t)it.w.seg_b * a.maxb + pidx] : -1;
-            if (m.id < 0 || m.id >= a.n_pages) {
-                report(a.status, VC_ERR_BAD_INDEX);
-                m.id = 0;
-            }
-            if (!m.is_v) {
-                const int64_t at = (int64_t)m.id * a.hkv + m.kvh;
-                m.sc = make_float2(a.ks[at], a.vs[at]);
-            }
-        }
-        return m;
-    };
-    // a lane's pieces of a page: row r0 (and r0 + 8), piece c0 (and, with 128-byte
-    // rows, c1): eight lanes read whole sectors and write different banks, half of
-    // one row and the other half of the next
-    const int r0 = lane >> 2, c0 = D == 128 ? (lane & 3) + 4 * (r0 & 1) : lane & 3, c1 = c0 ^ 4;
-    uint4 *mine = reinterpret_cast<uint4 *>(codes) + lane;  // [R][U][32]
-    auto copy = [&](int stage, const Item &m, int page) {
-        const int id = __shfl_sync(0xffffffffu, m.id, page);
-        const uint8_t *src = (m.is_v ? a.vc : a.kc) + ((int64_t)id * a.hkv + m.kvh) * (kPage * D) + r0 * D;
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            cp_async16(mine + (stage * U + k) * 32, src + k / IT * 8 * D + (IT == 2 && k % 2 ? c1 : c0) * 16);
-    };
-    // where the halves of piece c of row r0 go
-    auto place = [&](int c, int h) { return (c >> 2) * (BK * 128) + r0 * 128 + (((2 * c + h) & 7) ^ r0) * 16; };
-    const int to[2][2] = {{place(c0, 0), place(c0, 1)}, {place(c1, 0), place(c1, 1)}};
-    Item cur = fetch(), nxt = cur;
-    if (cur.there) {
-#pragma unroll
-        for (int p = 0; p < R; ++p) {
-            copy(p, cur, p);
-            cp_async_commit();
-        }
-        nxt = fetch();
-    }
-    for (; cur.there; seq += C::CONVERTERS) {
-        const uint32_t slot = seq / H % C::SLOTS, use = seq / H / C::SLOTS;
-        // (parity: this warp's last part had its place, so the block SLOTS before that is used up)
-        static_assert((C::CONVERTERS + H - 1) / H <= C::SLOTS, "phases that a parity tells apart");
-        if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], (use - 1) & 1, a.status, a.wait_ns))) break;
-        uint8_t *dst = skv + slot * C::SLOT + seq % H * (64 * 128);
-        if (!cur.is_v && lane < PG)
-            scales[(cur.k % kScaleRing * H + seq % H) * PG + lane] = make_float2(scale_of(cur.sc.x), scale_of(cur.sc.y));
-#pragma unroll 1
-        for (int p0 = 0; p0 < PG; p0 += R) {
-#pragma unroll
-            for (int p = 0; p < R; ++p) {
-                cp_async_wait<R - 1>();
-                uint4 u[U];
-#pragma unroll
-                for (int k = 0; k < U; ++k) u[k] = mine[(p * U + k) * 32];
-                // (a group each time, so that what is under way is counted in pages)
-                if (p0 + R < PG) copy(p, cur, p0 + R + p);
-                else if (nxt.there) copy(p, nxt, p);
-                cp_async_commit();
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int r = (p0 + p) * kPage + k / IT * 8;
-                    uint4 lo, hi;
-                    widen<E4M3>(u[k], lo, hi);
-                    if (r + r0 >= cur.rows) lo = hi = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][0] + r * 128) = lo;
-                    *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][1] + r * 128) = hi;
-                }
-            }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&full[slot]);
-        cur = nxt;
-        if (nxt.there) nxt = fetch();
-    }
-    cp_async_wait<0>();
-}
-
 template <int D, int QT, bool E4M3>
 __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
     using C = Tc<D, QT>;
@@ -251,11 +90,13 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
         if (threadIdx.x == 0) report(a.status, VC_ERR_UNSUPPORTED);
         return;
     }
-    uint8_t *sq = smem, *skv = smem + C::OFF_KV;
+    uint8_t *sq = smem, *skv = smem + C::OFF_KV, *scodes = smem + C::OFF_CODES;
     float2 *scales = reinterpret_cast<float2 *>(smem + C::OFF_SC);  // [kScaleRing][PG]
     uint64_t *q_ready = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [QT]
     uint64_t *s_ready = q_ready + QT, *p_ready = s_ready + C::NS, *o_done = p_ready + C::NBUF, *pv_done = o_done + QT;
-    uint64_t *full = pv_done + QT, *empty = full + C::SLOTS, *idle = empty + C::SLOTS;
+    uint64_t *full = pv_done + QT, *empty = full + C::SLOTS;           // blocks in fp16
+    uint64_t *full8 = empty + C::SLOTS, *empty8 = full8 + C::SLOTS8;   // blocks of codes
+    uint64_t *idle = empty8 + C::SLOTS8;
     uint32_t *tslot = reinterpret_cast<uint32_t *>(idle + 1);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -272,8 +113,12 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
         for (int i = 0; i < C::NS; ++i) mbar_init(&s_ready[i], 1);
         for (int i = 0; i < C::NBUF; ++i) mbar_init(&p_ready[i], 4);
         for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(&full[i], BK / 64);
+            mbar_init(&full[i], 2);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < C::SLOTS8; ++i) {
+            mbar_init(&full8[i], 1);
+            mbar_init(&empty8[i], 2);
         }
         mbar_init(idle, 1);
         fence_mbar_init();
@@ -302,6 +147,74 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
 
     if (warp >= C::SM_WARPS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == C::SM_WARPS) {
+        // ================= producer =================
+        if (!block_skips(a.skip_copies)) {
+            uint32_t seq = 0;   // copies into the ring so far
+            uint32_t blocks = 0;
+            while (alive && w.next(a)) {
+                const int32_t *trow = a.table + (int64_t)w.seg_b * a.maxb;
+                const int npages = ceil_div(w.seg_len, kPage);
+                // page ids, 32 at a time, one batch ahead; their scales half a batch later
+                // (pages behind the request's end: any valid page, masked and cleared)
+                constexpr int NB = 32 / PG;
+                bool nthere = false;
+                auto load_ids = [&](int i0) {
+                    const int i = i0 + lane / PG;
+                    int id = 0;
+                    nthere = false;
+                    if (i < w.seg_n) {
+                        const int pidx = (w.seg_blk + i) * PG + lane % PG;
+                        if (pidx < npages) {
+                            id = pidx < a.maxb ? trow[pidx] : -1;
+                            if (id < 0 || id >= a.n_pages) {
+                                report(a.status, VC_ERR_BAD_INDEX);
+                                id = 0;
+                            }
+                            nthere = true;
+                        }
+                    }
+                    return id;
+                };
+                auto load_scales = [&](int id) {
+                    const int64_t at = (int64_t)id * a.hkv + w.seg_kvh;
+                    return nthere ? make_float2(a.ks[at], a.vs[at]) : make_float2(1.0f, 0.0f);
+                };
+                auto copy = [&](int i, int ids, const CUtensorMap *map) {
+                    const int id = __shfl_sync(0xffffffffu, ids, (i % NB) * PG + lane % PG);
+                    const int y = (id * a.hkv + w.seg_kvh) * kPage;
+                    const int slot = seq % C::SLOTS8;
+                    const uint32_t use = seq / C::SLOTS8;
+                    if (use > 0)
+                        alive = __all_sync(0xffffffffu, mbar_wait(&empty8[slot], (use - 1) & 1, a.status, a.wait_ns));
+                    if (!alive) return;
+                    if (lane == 0) mbar_arrive_expect_tx(&full8[slot], C::SLOT8);
+                    __syncwarp();
+                    if (lane < PG) vtc::tma2d(scodes + slot * C::SLOT8 + lane * kPage * D, map, 0, y, &full8[slot]);
+                    ++seq;
+                };
+                int cur = 0, nxt = load_ids(0);
+                float2 sc{}, nsc = load_scales(nxt);
+                for (int i = 0; i < w.seg_n && alive; ++i, ++blocks) {
+                    if (i % NB == 0) {
+                        cur = nxt;
+                        sc = nsc;
+                        nxt = load_ids(i + NB);
+                    } else if (i % NB == NB / 2) {
+                        nsc = load_scales(nxt);
+                    }
+                    const int from = (i % NB) * PG + lane % PG;
+                    const float pk = __shfl_sync(0xffffffffu, sc.x, from), pv = __shfl_sync(0xffffffffu, sc.y, from);
+                    if (lane < PG) scales[blocks % kScaleRing * PG + lane] = make_float2(scale_of(pk), scale_of(pv));
+                    __syncwarp();
+                    copy(i, cur, &a.kmap);
+                    if (alive) copy(i, cur, &a.vmap);
+                }
+            }
+            // no copy may be under way when the CTA ends
+            for (uint32_t q = seq > C::SLOTS8 ? seq - C::SLOTS8 : 0; q < seq; ++q)
+                if (!mbar_wait(&full8[q % C::SLOTS8], (q / C::SLOTS8) & 1, a.status, kWaitNs)) break;
+        }
+    } else if (warp == C::SM_WARPS + 1) {
         // ================= MMA issue (the warp in step, one elected thread; see tree_tc.cuh) =================
         const uint64_t qd0 = vtc::sdesc(smem_u32(sq), 16, 1024);
         const uint64_t kd0 = vtc::sdesc(smem_u32(skv), 16, 1024), vd0 = vtc::sdesc(smem_u32(skv), BK * 128, 1024);
@@ -328,9 +241,8 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
                     par ^= 1;
                 }
             }
-        } kp{0, 0}, vp{0, 0}, pp{0, 0};
+        } kp{0, 0}, vp{1, 0}, pp{0, 0};
         uint32_t sb = 0, seg = 0;
-        int kt = 0;  // blocks of K behind kp
         auto wait1 = [&](uint64_t *bar, uint32_t par) {
             alive = __all_sync(0xffffffffu, mbar_wait(bar, par, a.status, a.wait_ns));
             return alive;
@@ -348,16 +260,13 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
             if (++sb == C::NBUF) sb = 0;
             if (t == QT - 1) {
                 tree::umma_commit(&empty[kp.i]);
-                kp.step(kt++ < C::LAG ? 1 : 2, C::SLOTS);
+                kp.step(2, C::SLOTS);
             }
         };
         for (;; ++seg) {
             const bool any = alive && w.next(a);
             const int n = __shfl_sync(0xffffffffu, any ? w.seg_n : 0, 0);
             if (n == 0) break;
-            kp = vp;  // (places in the ring follow the order of Items)
-            kt = 0;
-            vp.step(min(C::LAG + 1, n), C::SLOTS);
 #pragma unroll
             for (int i = 0; i < C::NBUF; ++i) {
                 if (i / QT >= n) break;
@@ -378,15 +287,63 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
                 }
                 if (!alive) break;
                 tree::umma_commit(&empty[vp.i]);
-                vp.step(j + 1 + C::LAG < n ? 2 : 1, C::SLOTS);
+                vp.step(2, C::SLOTS);
             }
         }
         // nor may a product be: TMEM is freed behind it
         tree::umma_commit(idle);
         mbar_wait(idle, 0, a.status, kWaitNs);
-    } else if (warp > C::SM_WARPS) {
-        convert<C, D, E4M3>(a, w, warp - C::SM_WARPS - 1, skv, smem + C::OFF_CODES + (warp - C::SM_WARPS - 1) * C::CODES, scales, full,
-                            empty);
+    } else if (warp >= C::SM_WARPS + 2) {
+        // ================= conversion: half a block's rows each =================
+        const int half = warp - (C::SM_WARPS + 2);
+        uint32_t seq = 0;
+        while (alive && w.next(a)) {
+            for (int i = 0; i < 2 * w.seg_n && alive; ++i, ++seq) {
+                const int slot = seq % C::SLOTS, slot8 = seq % C::SLOTS8;
+                alive = __all_sync(0xffffffffu, mbar_wait(&full8[slot8], (seq / C::SLOTS8) & 1, a.status, a.wait_ns));
+                if (alive && seq >= C::SLOTS)
+                    alive = __all_sync(0xffffffffu, mbar_wait(&empty[slot], (seq / C::SLOTS - 1) & 1, a.status, a.wait_ns));
+                if (!alive) break;
+                const uint8_t *src = scodes + slot8 * C::SLOT8;
+                uint8_t *dst = skv + slot * C::SLOT;
+                // rows of V behind the request's end: whatever they hold, 0 times it is to be 0
+                const int rows = i & 1 ? w.seg_len - (w.seg_blk + i / 2) * BK : BK;
+                // eight lanes read and write different banks: with 128-byte rows of codes
+                // half of one row and the other half of the next
+                constexpr int IT = D / 64, U = 4;  // passes over eight rows; pieces under way
+                constexpr int N = BK / 2 / 8 * IT;
+                auto place = [&](int k, int &r, int &c) {
+                    r = half * (BK / 2) + k / IT * 8 + (lane >> 2);
+                    c = D == 128 ? (lane & 3) + 4 * ((r & 1) ^ (k & 1)) : lane & 3;
+                };
+#pragma unroll 1
+                for (int k0 = 0; k0 < N; k0 += U) {
+                    uint4 u[U];
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        int r, c;
+                        place(k0 + k, r, c);
+                        u[k] = *reinterpret_cast<const uint4 *>(src + piece_at<D>(r, c));
+                    }
+#pragma unroll
+                    for (int k = 0; k < U; ++k) {
+                        int r, c;
+                        place(k0 + k, r, c);
+                        uint4 lo, hi;
+                        widen<E4M3>(u[k], lo, hi);
+                        if (r >= rows) lo = hi = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(dst + vtc::sw128(r, 2 * c, BK)) = lo;
+                        *reinterpret_cast<uint4 *>(dst + vtc::sw128(r, 2 * c + 1, BK)) = hi;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&full[slot]);
+                    mbar_arrive(&empty8[slot8]);
+                }
+            }
+        }
     } else {
         // ================= softmax: one thread per row =================
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFTMAX));

@@ -79,6 +79,20 @@ bool encode_pool(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A pool of 8-bit codes: boxes of 16 rows x D channels (a kv head's block of
+// one page), each row swizzled as a whole.
+bool encode_pool8(CUtensorMap *m, const void *pool, int64_t n_pages, int hkv, int d) {
+    EncodeTiled fn = encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)n_pages * hkv * kPage};
+    cuuint64_t strides[1] = {(cuuint64_t)d};
+    cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)kPage};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int verify_splits(int max_seq_len) { return max(1, ceil_div(ceil_div(max_seq_len, kPage), vtc::kSplitPages)); }
 
 bool verify_supported(const vc_kv_format &f, int hq, int n_q) {
