@@ -316,9 +316,12 @@ __device__ __forceinline__ void one_cta(const Args &a, uint8_t *smem) {
             }
             for (int j = 0; j < n && alive; ++j) {
                 const bool more = j + C::NBUF < n;
-                if (!wait1(&p_ready[pp.i], pp.par)) break;
-                if (!wait1(&full[vp.i], vp.par)) break;
-                if (more && !wait1(&full[kp.i], kp.par)) break;
+                if (!__all_sync(0xffffffffu, ready3(&p_ready[pp.i], pp.par, &full[vp.i], vp.par, more ? &full[kp.i] : &full[vp.i],
+                                                    more ? kp.par : vp.par))) {
+                    if (!wait1(&p_ready[pp.i], pp.par)) break;
+                    if (!wait1(&full[vp.i], vp.par)) break;
+                    if (more && !wait1(&full[kp.i], kp.par)) break;
+                }
                 vtc::tc_fence_after();
                 const uint64_t vd = vd0 + vp.i * (C::SLOT / 16);
 #pragma unroll

@@ -74,6 +74,22 @@ __device__ __forceinline__ void widen(const uint4 &u, uint4 &lo, uint4 &hi) {
     hi = make_uint4(to_f16_lo<E4M3>(z), to_f16_hi<E4M3>(z), to_f16_lo<E4M3>(w), to_f16_hi<E4M3>(w));
 }
 
+// Whether three phases are over, asked for at once: one after another a wait takes
+// the warp that issues products 130 cycles each, ready or not.
+__device__ __forceinline__ bool ready3(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb, uint64_t *c, uint32_t pc) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q, r;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 r, [%5], %6;\n\t"
+        "and.pred p, p, q;\n\tand.pred p, p, r;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc)
+        : "memory");
+    return ok != 0;
+}
+
 __device__ __forceinline__ void mul2(float &d0, float &d1, float b) {
     asm("{\n\t.reg .b64 ra, rb;\n\t"
         "mov.b64 ra, {%0, %1};\n\tmov.b64 rb, {%2, %2};\n\t"
@@ -248,6 +264,12 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
             return alive;
         };
         auto wait = [&](bool p, bool v, bool k, int q) {
+            if (p && q < 0 &&
+                __all_sync(0xffffffffu, ready3(&p_ready[pp.i], pp.par, v ? &full[vp.i] : &p_ready[pp.i], v ? vp.par : pp.par,
+                                               k ? &full[kp.i] : &p_ready[pp.i], k ? kp.par : pp.par))) {
+                vtc::tc_fence_after();
+                return true;
+            }
             if (p && !wait1(&p_ready[pp.i], pp.par)) return false;
             if (v && !wait1(&full[vp.i], vp.par)) return false;
             if (k && !wait1(&full[kp.i], kp.par)) return false;
