@@ -30,7 +30,7 @@ struct One {
     static constexpr int LAG = NBUF;  // S runs NBUF blocks ahead of P V
     static constexpr int STAGE = 8 * 4096;
     static constexpr int LIMIT = 226 * 1024;
-    static constexpr int CONVERTERS = 7, PAGES_AHEAD = 4, CODES = PAGES_AHEAD * kPage * D;  // each one's pages of codes under way
+    static constexpr int CONVERTERS = 7, CODES = BK * D;  // each one's codes under way
     static constexpr int FIT = (LIMIT - 8192 - STAGE - CONVERTERS * CODES) / SLOT;
     static constexpr int SLOTS = FIT < 16 ? FIT : 16;
     static_assert(SLOTS / 2 + LAG + 1 <= kScaleRing, "ring depth");
@@ -44,10 +44,10 @@ struct One {
     static constexpr int O_COL0 = NBUF * BK, Q_COL0 = O_COL0 + 2 * D;
     static_assert(Q_COL0 + D / 2 <= 512, "TMEM columns");
     // two groups of softmax warps; MMA issue and seven converters.
-    // (2 x 128 x 176 + 2 x 128 x 80 = 512 x 128 registers)
+    // (2 x 128 x 160 + 2 x 128 x 96 = 512 x 128 registers)
     static constexpr int SM_WARPS = 8, WARPS = 16, THREADS = WARPS * 32;
     static_assert(SM_WARPS + 1 + CONVERTERS == WARPS, "roles");
-    static constexpr int REGS_SOFTMAX = 176, REGS_OTHER = 80;
+    static constexpr int REGS_SOFTMAX = 160, REGS_OTHER = 96;
     static constexpr int ROWS = kTileRows;
 };
 
@@ -57,158 +57,168 @@ struct One {
 template <int BK, int LAG>
 struct Items {
     tree::Walk<BK> w;
-    int i = 0, n = 0;   // step of the segment's n + LAG, and whether V is its next
+    int i = 0, n = 0;   // step of the segment's n + LAG; v: its V was the last item
     bool v = true;
-    // the current item
-    int blk;
-    bool is_v;
+    int k0 = 0;         // blocks of the segments before
+    // the item: a block of its segment
+    int at = 0;
+    bool is_v = false;
     __device__ bool next(const Args &a) {
         for (;;) {
             if (v) {  // the next step
                 v = false;
                 if (n == 0 || ++i == n + LAG) {
+                    k0 += n;
+                    i = n = 0;
                     if (!w.next(a)) {
-                        n = 0;
                         v = true;
                         return false;
                     }
-                    i = 0;
                     n = w.seg_n;
                 }
                 if (i < n) {
-                    blk = w.seg_blk + i;
+                    at = i;
                     is_v = false;
                     return true;
                 }
             }
             v = true;
             if (i >= LAG) {
-                blk = w.seg_blk + i - LAG;
+                at = i - LAG;
                 is_v = true;
                 return true;
             }
         }
     }
+    // The item `by` further on.
+    __device__ bool skip(const Args &a, int by) {
+        const int q = 2 * i + v + by;
+        if (i >= LAG && q >> 1 < n) {  // (where K and V alternate)
+            i = q >> 1;
+            v = is_v = q & 1;
+            at = i - (v ? LAG : 0);
+            return true;
+        }
+        while (--by > 0)
+            if (!next(a)) return false;
+        return next(a);
+    }
 };
 
-// Converter warp `part` of C::CONVERTERS: every so many-th 64 keys from codes in
-// global memory to fp16 in the ring.  C::PAGES_AHEAD pages are under way by asynchronous
-// copies, each lane's pieces for itself alone.  (The SM's TMA unit takes copies
-// of a head block too slowly: 8 x 32768 keys 230 us; in registers they spill.)
-// The warps of a block of K leave the block's scales beside it.
+// Converter warp `part` of C::CONVERTERS: every so many-th block from codes in
+// global memory to fp16 in the ring.  A block's pages are under way by
+// asynchronous copies, each lane's pieces for itself alone.  (The SM's TMA unit
+// takes copies of a head block too slowly: 8 x 32768 keys 230 us; in registers
+// they spill.)  The warp of a block of K leaves the block's scales beside it.
 template <class C, int D, bool E4M3>
 __device__ __forceinline__ void convert(const Args &a, const tree::Walk<C::BK> &w, int part, uint8_t *skv, uint8_t *codes,
                                         float2 *scales, uint64_t *full, uint64_t *empty) {
-    constexpr int BK = C::BK, IT = D / 64, U = 2 * IT;  // pieces of a page that a lane holds
-    constexpr int H = BK / 64, PG = 4, R = C::PAGES_AHEAD;  // parts of a block, pages of a part
-    static_assert(PG % R == 0 && BK % 64 == 0, "pages of a part");
+    constexpr int BK = C::BK, PG = C::PG, IT = D / 64, U = 2 * IT;  // pieces of a page that a lane holds
     const int lane = threadIdx.x & 31;
     if (block_skips(a.skip_copies)) return;
     Items<BK, C::LAG> it;
     it.w = w;
-    int skip = part;
-    uint32_t seq = part, ahead = 0, ahead_k = 0;  // parts: this warp's, fetched; blocks of K so far
-    bool more = true;
+    uint32_t seq = part;  // this warp's item in the order
     struct Item {
         bool there, is_v;
-        int rows;         // rows of V that hold tokens; below it nothing is kept
-        int id;           // lane p: page p
-        float2 sc;        // lane p: its scales (of a block of K)
-        uint32_t k;       // blocks of K before
-        int kvh;
+        bool page;   // lane p: page p holds tokens
+        int rows;    // rows that hold tokens
+        int id;      // lane p: page p
+        float2 sc;   // lane p: its scales (of a block of K)
+        int k, kvh;  // block of the range
     };
-    auto fetch = [&]() {  // the next item of this warp
+    // this warp's item `by` further on, its page ids on their way; a turn later they
+    // are looked at and the scales set off, and used another turn later
+    bool more = true;
+    auto fetch = [&](int by) {
         Item m;
-        for (int s = 0; s <= skip && more; ++s, ++ahead) {
-            if (ahead % H) continue;
-            more = it.next(a);
-            if (more && !it.is_v) ++ahead_k;
-        }
+        more = more && it.skip(a, by);
         m.there = more;
-        m.k = ahead_k - 1;
-        const int half = (ahead - 1) % H;
-        skip = C::CONVERTERS - 1;
-        m.id = 0;
+        m.page = m.is_v = false;
+        m.id = m.rows = m.kvh = m.k = 0;
         m.sc = make_float2(1.0f, 0.0f);
-        if (!m.there) return m;
-        m.is_v = it.is_v;
-        m.rows = m.is_v ? it.w.seg_len - it.blk * BK - half * 64 : BK;
-        m.kvh = it.w.seg_kvh;
-        const int pidx = (it.blk * H + half) * PG + lane;
-        // (pages behind the request's end: any valid page, masked and cleared)
-        if (lane < PG && pidx * kPage < it.w.seg_len) {
-            m.id = pidx < a.maxb ? a.table[(int64_t)it.w.seg_b * a.maxb + pidx] : -1;
-            if (m.id < 0 || m.id >= a.n_pages) {
-                report(a.status, VC_ERR_BAD_INDEX);
-                m.id = 0;
-            }
-            if (!m.is_v) {
-                const int64_t at = (int64_t)m.id * a.hkv + m.kvh;
-                m.sc = make_float2(a.ks[at], a.vs[at]);
-            }
+        if (more) {
+            const int blk = it.w.seg_blk + it.at, pidx = blk * PG + lane;
+            m.is_v = it.is_v;
+            m.k = it.k0 + it.at;
+            m.rows = it.w.seg_len - blk * BK;
+            m.kvh = it.w.seg_kvh;
+            // (pages behind the request's end: any valid page, masked and cleared)
+            m.page = lane < PG && pidx * kPage < it.w.seg_len;
+            if (m.page) m.id = pidx < a.maxb ? a.table[(int64_t)it.w.seg_b * a.maxb + pidx] : -1;
         }
         return m;
+    };
+    auto look = [&](Item &m) {
+        if (m.id < 0 || m.id >= a.n_pages) {
+            report(a.status, VC_ERR_BAD_INDEX);
+            m.id = 0;
+        }
+        if (m.page && !m.is_v) {
+            const int64_t x = (int64_t)m.id * a.hkv + m.kvh;
+            m.sc = make_float2(a.ks[x], a.vs[x]);
+        }
     };
     // a lane's pieces of a page: row r0 (and r0 + 8), piece c0 (and, with 128-byte
     // rows, c1): eight lanes read whole sectors and write different banks, half of
     // one row and the other half of the next
     const int r0 = lane >> 2, c0 = D == 128 ? (lane & 3) + 4 * (r0 & 1) : lane & 3, c1 = c0 ^ 4;
-    uint4 *mine = reinterpret_cast<uint4 *>(codes) + lane;  // [R][U][32]
-    auto copy = [&](int stage, const Item &m, int page) {
+    uint4 *mine = reinterpret_cast<uint4 *>(codes) + lane;  // [PG][U][32]
+    auto copy = [&](const Item &m, int page) {
         const int id = __shfl_sync(0xffffffffu, m.id, page);
         const uint8_t *src = (m.is_v ? a.vc : a.kc) + ((int64_t)id * a.hkv + m.kvh) * (kPage * D) + r0 * D;
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            cp_async16(mine + (stage * U + k) * 32, src + k / IT * 8 * D + (IT == 2 && k % 2 ? c1 : c0) * 16);
+            cp_async16(mine + (page * U + k) * 32, src + k / IT * 8 * D + (IT == 2 && k % 2 ? c1 : c0) * 16);
     };
     // where the halves of piece c of row r0 go
     auto place = [&](int c, int h) { return (c >> 2) * (BK * 128) + r0 * 128 + (((2 * c + h) & 7) ^ r0) * 16; };
     const int to[2][2] = {{place(c0, 0), place(c0, 1)}, {place(c1, 0), place(c1, 1)}};
-    Item cur = fetch(), nxt = cur;
+    Item cur = fetch(part + 1), nxt = fetch(C::CONVERTERS), after = fetch(C::CONVERTERS);
+    look(cur);
+    look(nxt);
     if (cur.there) {
 #pragma unroll
-        for (int p = 0; p < R; ++p) {
-            copy(p, cur, p);
+        for (int p = 0; p < PG; ++p) {
+            copy(cur, p);
             cp_async_commit();
         }
-        nxt = fetch();
     }
     for (; cur.there; seq += C::CONVERTERS) {
-        const uint32_t slot = seq / H % C::SLOTS, use = seq / H / C::SLOTS;
-        // (parity: this warp's last part had its place, so the block SLOTS before that is used up)
-        static_assert((C::CONVERTERS + H - 1) / H <= C::SLOTS, "phases that a parity tells apart");
+        const uint32_t slot = seq % C::SLOTS, use = seq / C::SLOTS;
+        // (parity: this warp's last block had its place, so the one SLOTS before that is used up)
+        static_assert(C::CONVERTERS <= C::SLOTS, "phases that a parity tells apart");
         if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[slot], (use - 1) & 1, a.status, a.wait_ns))) break;
-        uint8_t *dst = skv + slot * C::SLOT + seq % H * (64 * 128);
+        uint8_t *dst = skv + slot * C::SLOT;
         if (!cur.is_v && lane < PG)
-            scales[(cur.k % kScaleRing * H + seq % H) * PG + lane] = make_float2(scale_of(cur.sc.x), scale_of(cur.sc.y));
-#pragma unroll 1
-        for (int p0 = 0; p0 < PG; p0 += R) {
+            scales[cur.k % kScaleRing * PG + lane] = make_float2(scale_of(cur.sc.x), scale_of(cur.sc.y));
 #pragma unroll
-            for (int p = 0; p < R; ++p) {
-                cp_async_wait<R - 1>();
-                uint4 u[U];
+        for (int p = 0; p < PG; ++p) {
+            cp_async_wait<PG - 1>();
+            uint4 u[U];
 #pragma unroll
-                for (int k = 0; k < U; ++k) u[k] = mine[(p * U + k) * 32];
-                // (a group each time, so that what is under way is counted in pages)
-                if (p0 + R < PG) copy(p, cur, p0 + R + p);
-                else if (nxt.there) copy(p, nxt, p);
-                cp_async_commit();
+            for (int k = 0; k < U; ++k) u[k] = mine[(p * U + k) * 32];
+            // (a group each time, so that what is under way is counted in pages)
+            if (nxt.there) copy(nxt, p);
+            cp_async_commit();
 #pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    const int r = (p0 + p) * kPage + k / IT * 8;
-                    uint4 lo, hi;
-                    widen<E4M3>(u[k], lo, hi);
-                    if (r + r0 >= cur.rows) lo = hi = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][0] + r * 128) = lo;
-                    *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][1] + r * 128) = hi;
-                }
+            for (int k = 0; k < U; ++k) {
+                const int r = p * kPage + k / IT * 8;
+                uint4 lo, hi;
+                widen<E4M3>(u[k], lo, hi);
+                // V behind the request's end: whatever it holds, 0 times it is to be 0
+                if (cur.is_v && r + r0 >= cur.rows) lo = hi = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][0] + r * 128) = lo;
+                *reinterpret_cast<uint4 *>(dst + to[IT == 2 && k % 2][1] + r * 128) = hi;
             }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[slot]);
         cur = nxt;
-        if (nxt.there) nxt = fetch();
+        nxt = after;
+        look(nxt);
+        after = fetch(C::CONVERTERS);
     }
     cp_async_wait<0>();
 }
