@@ -31,6 +31,11 @@
  * verification pass), vc_tree_accept, vc_tree_commit, and vc_token_logprobs
  * (log probabilities, entropy and the alternatives a tree is drawn from).
  *
+ * A draft cache that is nearly lossless is held in 8 bits (vc_kv8_write,
+ * vc_kv8_attn: one token, a block or a tree of them), and the block tables of
+ * all caches are made and kept by vc_pages_free, vc_pages_fork,
+ * vc_pages_reserve, vc_pages_compact and vc_pages_copy.
+ *
  * Conventions
  *  - Every pointer argument named as "device" must point to device memory of
  *    the current device; "host" pointers to host memory.  The caller owns and
@@ -804,7 +809,8 @@ VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, con
  * and out on 16-byte boundaries.  A request with seq_lens[b] = 0 is idle: zeros.
  * One with fewer than n_q tokens, or more than max_seq_len or max_blocks
  * pages, gets zeros and VC_ERR_BAD_INDEX; a row whose keys did not all arrive
- * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT.
+ * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT (more than
+ * 16 rows of a kv head, 32 with head_dim 64; fewer are served without waits).
  * Codes are exact in the products' type (fp16), and q is taken times a power
  * of two for each row that fits it there; probabilities enter the second product in fp16
  * (each off by at most 2^-11 of itself, or 2^-25 of the largest beside V's
@@ -935,17 +941,18 @@ VC_API vc_status vc_pages_copy(const vc_page_array *arrays, int32_t n_arrays, in
  * use).  Every wait of a kernel on a copy or on another warp gives up after
  * a time limit, reports VC_ERR_TIMEOUT in dev_status and lets the block
  * drain and exit (no GPU hang on a lost copy).  This sets that limit for the
- * draft, draft-step, verification, mixed, tree-attention and (rows of more
- * than about 4 KB) token-log-probability launches made after the call:
+ * draft, draft-step, verification, mixed, tree-attention, 8-bit-attention (of
+ * more than 16 rows a kv head, 32 with head_dim 64) and (rows of more than about
+ * 4 KB) token-log-probability launches made after the call:
  * wait_limit_ns in (0, 2e9], or 0 for the default of 2 s.  skip_copies != 0
  * makes those kernels issue none of their copies (and signal none), so every
  * wait on a copy runs into the limit: attention outputs are then zeros and
  * nothing of the cache is read; log probabilities are as vc_token_logprobs
- * says.  skip_copies == 2: of a tree-attention or token-log-probability
- * launch only the blocks of odd index do so.  A short limit with skip_copies
- * == 0 is for these two alone, whose blocks end after the copies that they
- * issued: those of the other kernels do not wait for them once a wait has run
- * out.  Calls racing with launches on other threads see either setting.
+ * says.  skip_copies == 2: of a tree-attention, 8-bit-attention or
+ * token-log-probability launch only the blocks of odd index do so.  A short
+ * limit with skip_copies == 0 is for these three alone, whose blocks end after
+ * the copies that they issued: those of the other kernels do not wait for them
+ * once a wait has run out.  Calls racing with launches on other threads see either setting.
  * VC_ERR_INVALID_ARG for a limit out of range.
  */
 VC_API vc_status vc_debug_set_wait_fault(int64_t wait_limit_ns, int32_t skip_copies);

@@ -22,6 +22,11 @@ written at slots of their own), ``tree_plan`` (masks and positions),
 ``tree_attn`` (the tree over KV_full), ``tree_accept`` / ``tree_commit`` (the
 greedy walk, the accepted path kept) and ``token_logprobs`` (log
 probabilities, entropy and the alternatives a tree is drawn from).
+
+An 8-bit cache: ``kv8_write`` (pages of KV_full quantised with a scale each) and
+``kv8_attn`` (one token, a block or a tree over it).  Pages of a pool, for any
+cache: ``pages_reserve`` (room, and a shared page's copy before it is written
+to), ``pages_fork``, ``pages_free``, ``pages_compact`` and ``pages_copy``.
 """
 from __future__ import annotations
 

@@ -45,8 +45,8 @@ bool supported(const vc_paged_kv8 &kv, int n_q, int hq) {
 
 // Rows that go to kv8_few.cuh at most.  More go to kv8_one.cuh, whose time
 // hardly depends on their number (8 x 32768 keys, head_dim 128: 16 rows 112 us
-// in the first, 169 in the second; 20 rows 276 and 171: so many accumulators leave a scheduler
-// two warps.  head_dim 64: 32 rows 105 and 144 us).
+// in the first, 158 in the second; 20 rows 276 and 160: so many accumulators
+// leave a scheduler two warps.  head_dim 64: 32 rows 104 and 125 us).
 constexpr int few_rows(int d) { return d == 64 ? 32 : 16; }
 
 // How a call is laid out over the GPU.

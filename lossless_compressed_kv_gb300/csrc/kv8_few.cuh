@@ -11,8 +11,12 @@
 //   S^T = K Q^T      16 keys x 8 rows, D / 16 steps
 //   O^T += V^T P^T   D / 16 tiles of 16 channels x 8 rows
 // With few rows the 128-row instructions of tcgen05 would spend their time on
-// rows that are not there (an instruction with M = 128 takes as long for four
-// rows), while these spend an instruction on 128 codes.
+// rows that are not there (kv8_one.cuh takes 155 us for four rows), while these
+// spend an instruction on 128 codes.
+// 8 x 32768 keys, 8 heads of 128: 4 rows 98 us (0.81 of measured HBM), 16 rows
+// 112; 4 x 131072 keys, 8 rows 179 (0.89).  Chains of shared-memory loads,
+// products and conversions bound it: a scheduler's four warps issue in 0.45 of the
+// cycles.
 //
 // A product of K and Q may take channels in any order, if both take the same:
 // a lane reads 16-byte pieces of a key's row and feeds four channels of them

@@ -1,14 +1,18 @@
 // Attention over an 8-bit cache for up to 128 rows, on the 5th-generation
-// tensor cores: memory is to bound it, so the chain S -> softmax -> P V of a
-// block must not.  Two groups of softmax warps take blocks in turn, each with
-// a maximum, a sum and an O of its own for the same rows, and S runs NBUF
-// blocks ahead; at a segment's end the two are put together.  (Two CTAs an SM
-// with one S buffer each, as tree_tc.cuh has it for bf16: 8 x 32768 keys, 128
-// rows 178 us.)
+// tensor cores.  Codes become fp16 in shared memory as in kv8_tc.cuh, here by
+// seven warps that fetch them by asynchronous copies; S runs NBUF blocks of 64
+// keys ahead, and two groups of softmax warps take blocks in turn, each with a
+// maximum, a sum and an O of its own for the same rows: at a segment's end the
+// two are put together.
 //
-// Per 128 keys and 128 rows (head_dim 128) the tensor core needs about 1570
-// cycles (an instruction of S takes 64 for its A operand, whatever N is), shared
-// memory and exponentials 1024 each, HBM 1394.
+// 8 x 32768 keys, 8 heads of 128, 128 rows: 172 us, 80 of which HBM needs; of
+// 4 rows it would take 155.  What bounds it is the warp that issues products
+// (about 50 cycles for each of a block's twelve, 40 for each of four commits, 130
+// for the wait), while the tensor pipe works a third of the time.  Measured
+// against it: two CTAs an SM with a chain of one S buffer each 178 us; codes
+// through a ring filled by TMA 230; S and P V issued by a warp each, which must
+// then wait for one another's products, 222 (head_dim 64: 129, where this takes
+// 130).
 //
 // Steps are blocks: step i uses S buffer i % NBUF and O i % 2.  A finished
 // S (i) was issued behind P V (i - NBUF): the P V before of the same O, step

@@ -8,8 +8,11 @@
 // in fp16 are all that is rounded; e4m3 products of Q and P split in two would
 // need as many instructions and more softmax arithmetic, and not serve int8.
 // What it costs is shared memory: 32 KB of codes (128 keys, head_dim 128) are
-// written, read, written again as 64 KB and read by each tile.  At 128 bytes a
-// cycle that takes 1536 cycles for one tile, where HBM takes 1394.
+// written, read, written again as 64 KB and read by each tile, with Q: 320 KB for
+// two tiles, 2500 cycles where the products take 2180.
+// 8 x 32768 keys, 256 rows 283 us (1016 TFLOP/s of products), 320 rows 407; seven
+// warps that fetch codes themselves, as in kv8_one.cuh, took 360 and 448 (the
+// ring of fp16 blocks is then too short, and the softmax warps spill).
 //
 // K's scales join the softmax scale, a factor a page; V's go with the
 // probabilities, relative to a reference (kv8.cuh) that moves like the running

