@@ -805,8 +805,8 @@ VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, con
  *  max_seq_len  host: bound of every seq_lens[b]
  *  workspace    vc_kv8_workspace_bytes, on a 32-byte boundary (calls that may
  *               run at the same time take one each)
- * 1 <= n_q <= 64, num_q_heads / num_kv_heads <= 8, softmax_scale > 0; codes, q
- * and out on 16-byte boundaries.  A request with seq_lens[b] = 0 is idle: zeros.
+ * 1 <= n_q <= 64, num_q_heads / num_kv_heads <= 8, softmax_scale > 0, num_pages
+ * * num_kv_heads < 2^27; codes, q and out on 16-byte boundaries.  A request with seq_lens[b] = 0 is idle: zeros.
  * One with fewer than n_q tokens, or more than max_seq_len or max_blocks
  * pages, gets zeros and VC_ERR_BAD_INDEX; a row whose keys did not all arrive
  * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT (more than
