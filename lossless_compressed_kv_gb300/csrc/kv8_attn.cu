@@ -1,4 +1,5 @@
 // vc_kv8_attn: attention over a cache held in 8 bits (see kv8.cuh).
+#include <atomic>
 #include <cmath>
 
 #include "kv8_one.cuh"
@@ -99,10 +100,14 @@ cudaError_t launch_few(const kv8::Args &a, cudaStream_t st) {
 template <class C, int D, void (*kernel)(kv8::Args)>
 cudaError_t launch_tiles(const kv8::Args &a, cudaStream_t st) {
     // the warps share out the registers that the block is launched with
-    static const int regs = [] {
+    static std::atomic<int> known{0};
+    int regs = known.load();
+    if (regs == 0) {
         cudaFuncAttributes f;
-        return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-    }();
+        const cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+        if (e != cudaSuccess) return e;
+        known.store(regs = f.numRegs);
+    }
     if (regs * C::WARPS < C::REGS_SOFTMAX * C::SM_WARPS + C::REGS_OTHER * (C::WARPS - C::SM_WARPS))
         return cudaErrorInvalidConfiguration;
     cudaError_t e = set_smem_limit((const void *)kernel, C::SMEM);
