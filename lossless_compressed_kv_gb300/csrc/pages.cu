@@ -117,12 +117,15 @@ struct Reserve {
     int32_t *count, *last;  // [pages]: writers of a shared page, the last of them
     int32_t *fresh;         // [pages]: the free pages to be taken, lowest first
     int32_t *first;         // [batch + 1]: pages taken by the rows before
-    int32_t *anew;          // [batch]: shared pages that the row replaces
+    int32_t *anew;          // [batch]: shared pages that the row replaces, or kRefused
     int32_t *status;
 };
 
+constexpr int kRefused = -1;
+
 // The pages of a row that is to hold positions [len, want): j0 .. j1 - 1 are
-// held already and written to, up to `goal` are needed.
+// held already and written to, up to `goal` are needed.  ok: so far as the
+// lengths tell.
 struct Span {
     int j0, j1, have, goal;
     bool writes, ok;
@@ -137,11 +140,16 @@ __device__ inline Span span_of(const Reserve &a, int b) {
     s.goal = max(have, need);
     s.j0 = len / kPage;
     s.j1 = min(have, need);
-    for (int j = s.j0; j < s.j1; ++j) {
-        const int p = a.m.table[(int64_t)b * a.m.maxb + j];
-        s.ok &= p >= 0 && p < a.m.n_pages && a.m.refs[p] > 0;
+    return s;
+}
+// The same of a row that has been looked at: whether it is served was settled
+// by the state that the call found, which handing out pages changes.
+__device__ inline Span settled(const Reserve &a, int b) {
+    Span s = span_of(a, b);
+    if (a.anew[b] == kRefused) {
+        s.ok = false;
+        s.j1 = s.j0;
     }
-    if (!s.ok) s.j1 = s.j0;
     return s;
 }
 // Whether row b takes a new page in place of p, which others hold as well: not
@@ -157,9 +165,19 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const __grid_co
     __shared__ int64_t wide[32];
     const Map &m = a.m;
     const int tid = threadIdx.x, lane = tid & 31;
+    // ---- rows that are refused ----
+    for (int b = tid; b < m.batch; b += kThreads) {
+        Span s = span_of(a, b);
+        for (int j = s.j0; j < s.j1; ++j) {
+            const int p = m.table[(int64_t)b * m.maxb + j];
+            s.ok &= p >= 0 && p < m.n_pages && m.refs[p] > 0;
+        }
+        if (!s.ok) report(a.status, VC_ERR_BAD_INDEX);
+        a.anew[b] = s.ok ? 0 : kRefused;
+    }
     // ---- the writers of each shared page ----
     for (int b = tid; b < m.batch; b += kThreads) {
-        const Span s = span_of(a, b);
+        const Span s = settled(a, b);
         for (int j = s.j0; j < s.j1; ++j) {
             const int p = m.table[(int64_t)b * m.maxb + j];
             a.count[p] = 0;
@@ -169,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const __grid_co
     if (tid == 0) upto_s = 0;
     __syncthreads();
     for (int b = tid; b < m.batch; b += kThreads) {
-        const Span s = span_of(a, b);
+        const Span s = settled(a, b);
         for (int j = s.j0; j < s.j1; ++j) {
             const int p = m.table[(int64_t)b * m.maxb + j];
             atomicAdd(&a.count[p], 1);
@@ -183,12 +201,13 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const __grid_co
         const int b = b0 + tid;
         int64_t need = 0;
         if (b < m.batch) {
-            const Span s = span_of(a, b);
-            if (!s.ok) report(a.status, VC_ERR_BAD_INDEX);
-            int n = 0;
-            for (int j = s.j0; j < s.j1; ++j) n += replaces(a, b, m.table[(int64_t)b * m.maxb + j]);
-            a.anew[b] = n;
-            need = s.ok ? n + s.goal - s.have : 0;
+            const Span s = settled(a, b);
+            if (s.ok) {
+                int n = 0;
+                for (int j = s.j0; j < s.j1; ++j) n += replaces(a, b, m.table[(int64_t)b * m.maxb + j]);
+                a.anew[b] = n;
+                need = n + s.goal - s.have;
+            }
         }
         int64_t all;
         const int64_t upto = block_scan(need, wide, all);
@@ -218,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const __grid_co
     const int room = min(found, asked);
     // ---- the rows that find all of theirs: first the pages that they replace ----
     for (int b = tid; b < m.batch; b += kThreads) {
-        const Span s = span_of(a, b);
+        const Span s = settled(a, b);
         const bool ok = s.ok && (!s.writes || a.first[b + 1] <= room);
         int from = -1, to = -1;
         if (ok && s.writes) {

@@ -55,8 +55,10 @@ class Map:
             lens[d] = lens[s]
 
     def reserve(self, lens, want):
-        """(granted, copy_src, copy_dst), row by row."""
+        """(granted, copy_src, copy_dst), row by row; which rows are refused
+        follows from the state that the call finds."""
         rows, width = self.table.shape
+        nobody = {p for p in range(len(self.refs)) if self.refs[p] <= 0}
         granted, src, dst = [0] * rows, [-1] * rows, [-1] * rows
         stopped = False
         for b in range(rows):
@@ -69,7 +71,7 @@ class Map:
                 self.bad = True
                 continue
             span = range(n // PAGE, min(have, need))
-            if not all(self.held(self.table[b, j]) and self.refs[self.table[b, j]] > 0 for j in span):
+            if not all(self.held(self.table[b, j]) and self.table[b, j] not in nobody for j in span):
                 self.bad = True
                 continue
             if stopped:
