@@ -870,8 +870,9 @@ VC_API vc_status vc_pages_free(const vc_page_map *map, const int32_t *keep, int3
  *  src, dst  device int32 [n]: rows; -1 beside -1 is no pair.  A row may be
  *            the source of many.
  * A pair whose row is out of range, whose target holds pages, is named as a
- * target twice or is a source as well, or whose source holds too few pages is
- * left out and reported (VC_ERR_BAD_INDEX).
+ * target twice or is a source as well, or whose source holds too few pages or,
+ * among those to be shared, a page out of range or that nobody holds is left
+ * out and reported (VC_ERR_BAD_INDEX).
  */
 VC_API vc_status vc_pages_fork(const vc_page_map *map, int32_t *seq_lens, const int32_t *src, const int32_t *dst,
                                int32_t n, int32_t *dev_status, vc_stream_t stream);

@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(256) pages_fork_kernel(Map m, int32_t *lens, c
         bad = len < 0 || have > m.blocks[s] || have > m.maxb || m.blocks[d] != 0;
         for (int j = threadIdx.x; j < have && !bad; j += blockDim.x) {
             const int p = m.table[(int64_t)s * m.maxb + j];
-            bad = p < 0 || p >= m.n_pages;
+            // (other pairs add references meanwhile, but to pages that have some)
+            bad = p < 0 || p >= m.n_pages || m.refs[p] <= 0;
         }
     }
     if (__syncthreads_or(bad)) {

@@ -46,7 +46,7 @@ class Map:
             ok = ok and sum(e == d for _, e in pairs) == 1 and all(e != d for e, _ in pairs)
             n = pages_for(int(lens[s])) if ok else 0
             ok = ok and lens[s] >= 0 and n <= before[s] and n <= self.table.shape[1] and before[d] == 0
-            if not ok or not all(self.held(p) for p in self.table[s, :n]):
+            if not ok or not all(self.held(p) and self.refs[p] > 0 for p in self.table[s, :n]):
                 self.bad = True
                 continue
             self.table[d, :n] = self.table[s, :n]

@@ -20,3 +20,22 @@ def test_reserve_refuses_a_page_that_the_same_call_hands_out(at):
     want[0], want[at], want[at + 1] = 6, 33, 20
     b.reserve([5 * h for h in held], want)
     assert b.o.bad and b.o.blocks[at] == 1 and b.o.blocks[at + 1] == 2
+
+
+@pytest.mark.parametrize("n", [1, 17, 300])
+def test_fork_refuses_a_page_that_nobody_holds(n):
+    """Page n + 2 of row 0 is free by its count; it stays so, however many pairs name it, and page 1 of
+    row 1, also in row 0, is shared by the pairs of row 1 alone."""
+    pages = list(range(n + 2)) + [n + 2]
+    table = [pages, [1] + [-1] * (n + 2)] + [[-1] * (n + 3) for _ in range(2 * n)]
+    refs = [1] * (n + 2) + [0, 0]
+    refs[1] = 2
+    b = Both(table, [n + 3, 1] + [0] * (2 * n), refs)
+    lens = [16 * (n + 3) - 4, 9] + [0] * (2 * n)
+    b.fork(lens, [0, 1] * n, list(range(2, 2 * n + 2)))
+    assert b.o.bad and b.o.refs[n + 2] == 0 and b.o.refs[1] == 2 + n and b.o.refs[0] == 1
+    b.st.zero_()
+    b.o.bad = False
+    lens[0] = 16 * (n + 2)                       # without that page the row can be shared
+    b.fork(lens, [0], [2])
+    assert not b.o.bad and lens[2] == lens[0]

@@ -9,3 +9,10 @@ def test_reserve_refuses_a_page_that_the_same_call_hands_out():
     assert m.bad and granted == [1, 1, 0] and (src, dst) == ([0, -1, -1], [1, -1, -1])
     assert m.blocks.tolist() == [1, 1, 1] and m.table.tolist() == [[1, -1, -1], [0, -1, -1], [1, -1, -1]]
     assert m.refs.tolist() == [1, 1, 0, 0, 0]
+
+
+def test_fork_refuses_a_page_that_nobody_holds():
+    m = P.Map([[0, 1], [2, -1], [-1, -1], [-1, -1]], [2, 1, 0, 0], [1, 0, 1])
+    lens = [20, 5, 0, 0]
+    m.fork(lens, [0, 1], [2, 3])
+    assert m.bad and m.refs.tolist() == [1, 0, 2] and m.blocks.tolist() == [2, 1, 0, 1] and lens == [20, 5, 0, 5]
