@@ -69,19 +69,31 @@ __global__ void __launch_bounds__(kWarps * 32, 4) kv8_write_kernel(const __grid_
             if (first < 0 || len < 0 || len > a.max_len) report(a.status, VC_ERR_BAD_INDEX);
         }
     }
-    // page k of those of all requests, found from page `at` of request b on
-    int b = 0, at = 0, n = pages_of(a, 0);
     const int per = 2 * a.hkv;  // blocks of a page
-    int total = 0;
-    for (int i = lane; i < a.batch; i += 32) total += pages_of(a, i);
+    // 32 requests, a lane each, from request b0 on: pages of the request, those up to and with
+    // it, and those before all of them
+    int b0 = 0, n = lane < a.batch ? pages_of(a, lane) : 0, upto = n, before = 0, total = n;
+    for (int i = lane + 32; i < a.batch; i += 32) total += pages_of(a, i);
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     const int64_t items = (int64_t)total * per;
+    if (me >= items) return;
+    auto sum = [&]() {
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+    };
+    sum();
     for (int64_t item = me; item < items; item += n_warps) {
         const int k = (int)(item / per), kind = (int)(item % per), h = kind >> 1;
-        while (k >= at + n) {  // (k < total: such a request is there)
-            at += n;
-            n = pages_of(a, ++b);
+        unsigned here;  // (k < total: such a request is there)
+        while ((here = __ballot_sync(0xffffffffu, k < before + upto)) == 0) {
+            before += __shfl_sync(0xffffffffu, upto, 31);
+            b0 += 32;
+            n = upto = b0 + lane < a.batch ? pages_of(a, b0 + lane) : 0;
+            sum();
         }
+        const int b = b0 + __ffs(here) - 1, at = before + __shfl_sync(0xffffffffu, upto - n, b - b0);
         const bool is_v = kind & 1;
         const int len = a.lens[b], pg = (a.first ? a.first[b] : 0) / kPage + k - at;
         const int src = pg < a.f_maxb ? a.f_table[(int64_t)b * a.f_maxb + pg] : -1;
