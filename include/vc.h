@@ -773,7 +773,10 @@ typedef struct {
  *   top = 448 (e4m3) or 127 (int8)
  *   scale = max(max |x| * fp32(1 / top), 2^-126),  r = 1 / scale
  *   code = x * r, limited to [-top, top], rounded to nearest even
- * Slots behind the last token get code 0.  Infinities take no part in the
+ * Slots behind the last token get code 0.  Of a page of dst that several
+ * requests hold at the same place (vc_pages_fork; KV_full's page is theirs
+ * alike) the tokens are those of the longest of them, whichever of them make
+ * it anew: rows of unequal lengths do not lose one another's.  Infinities take no part in the
  * scale and get the largest code, NaN code 0; either is reported
  * (VC_ERR_INVALID_ARG in dev_status).
  *  full         bits == 16, head_dim 64 or 128; pools on 16-byte boundaries

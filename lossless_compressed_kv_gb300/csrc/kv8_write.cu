@@ -7,7 +7,8 @@
 // bounds it (64750 tokens of 8 heads of 128, K and V: 63 us, 0.94 of measured HBM).  The blocks of all requests, laid end to end, are dealt out in
 // equal ranges to the warps of a grid that fills the GPU once: neighbouring
 // warps take neighbouring heads, and a call with one new page a request costs
-// no more than its pages.
+// no more than its pages.  A page that several requests hold is made from the
+// longest of them by each (holder_of).
 #include "vc_internal.cuh"
 
 namespace vc {
@@ -32,6 +33,27 @@ __device__ inline int pages_of(const WriteArgs &a, int b) {
     const int len = a.lens[b], first = a.first ? a.first[b] : 0;
     if (first < 0 || len < 0 || len > a.max_len) return 0;
     return first >= len ? 0 : ceil_div(len, kPage) - first / kPage;
+}
+
+// The request whose tokens page `dst`, the pg-th of request b, is made of: the
+// one with the most tokens in it (the first of those) among all that hold it
+// there.  By a warp; `left`: b's tokens in it, then the holder's.  Holders of
+// unequal lengths write the same page in one call, in no order, so each of
+// them writes what the longest one does.  (Looked for where b's tokens end in
+// the page: a full one holds all there are.)
+__device__ inline int holder_of(const WriteArgs &a, int b, int pg, int dst, int lane, int &left) {
+    int most = left, who = b;
+    for (int r = lane; r < a.batch; r += 32) {
+        const int len = a.lens[r], n = len <= a.max_len ? min(len - pg * kPage, kPage) : 0;
+        if (n > most && a.d_table[(int64_t)r * a.d_maxb + pg] == dst) {
+            most = n;
+            who = r;
+        }
+    }
+    const int top = __reduce_max_sync(0xffffffffu, most);
+    if (top == left) return b;
+    left = top;
+    return __reduce_min_sync(0xffffffffu, most == top ? who : INT32_MAX);
 }
 
 // Two magnitudes (bf16, as whole numbers) that are infinite or NaN.
@@ -96,14 +118,18 @@ __global__ void __launch_bounds__(kWarps * 32, 4) kv8_write_kernel(const __grid_
         const int b = b0 + __ffs(here) - 1, at = before + __shfl_sync(0xffffffffu, upto - n, b - b0);
         const bool is_v = kind & 1;
         const int len = a.lens[b], pg = (a.first ? a.first[b] : 0) / kPage + k - at;
-        const int src = pg < a.f_maxb ? a.f_table[(int64_t)b * a.f_maxb + pg] : -1;
+        int left = len - pg * kPage;  // rows of the page that hold tokens
         const int dst = pg < a.d_maxb ? a.d_table[(int64_t)b * a.d_maxb + pg] : -1;
+        int src = pg < a.f_maxb ? a.f_table[(int64_t)b * a.f_maxb + pg] : -1;
+        if (left < kPage && pg < a.d_maxb) {
+            const int from = holder_of(a, b, pg, dst, lane, left);
+            if (from != b) src = pg < a.f_maxb ? a.f_table[(int64_t)from * a.f_maxb + pg] : -1;
+        }
         if (src < 0 || src >= a.f_pages || dst < 0 || dst >= a.d_pages) {
             if (lane == 0) report(a.status, VC_ERR_BAD_INDEX);
             continue;
         }
         const uint4 *x = reinterpret_cast<const uint4 *>((is_v ? a.vp : a.kp) + ((int64_t)src * a.hkv + h) * kPage * D * 2);
-        const int left = len - pg * kPage;  // rows of the page that hold tokens
         uint4 u[P][2];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
