@@ -88,13 +88,18 @@ __device__ __forceinline__ unsigned long long mask_of(const Args &a, int b, int 
     return a.mask ? a.mask[(int64_t)b * a.n_q + i] & (~0ull >> (64 - a.n_q)) : ~0ull >> (63 - i);
 }
 
+// Warps that share a row of a unit of so many ranges: one reads eight at once.
+__host__ __device__ inline int join_warps(int ranges) { return ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8; }
+
 // Join the partials of units that span several ranges, and write zeros for
-// requests that are refused.  One block per (unit, kJoinWarps / W rows): W
-// warps share a row and take every W-th range each, eight partials read at
-// once, in an order that the lengths alone fix.
+// requests that are refused.  A unit's blocks (gridDim.y) go through its rows,
+// W warps to a row, each of which takes every W-th range, eight partials read
+// at once.  W follows from the unit's own ranges, so the order of the sums is
+// fixed by the lengths alone: not by the bound that the call is given for
+// them, from which the grid follows.
 constexpr int kJoinWarps = 8;
 template <int D, int BK>
-__device__ __forceinline__ void join_block(const Args &a, int W, int lane_rows) {
+__device__ __forceinline__ void join_block(const Args &a, int lane_rows) {
     constexpr int E = D / 32, U = 8;
     __shared__ float part[kJoinWarps][E + 2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -108,92 +113,97 @@ __device__ __forceinline__ void join_block(const Args &a, int W, int lane_rows) 
     const int u0 = before * a.hkv + kvh * nblk;
     const int g0 = nblk > 0 ? deal.group_of(u0) : 0, g1 = nblk > 0 ? deal.group_of(u0 + nblk - 1) : -1;
     if (nblk > 0 && g0 == g1) return;  // finished there
-    const int rg = blockIdx.y * (kJoinWarps / W) + warp / W;
-    const bool row_ok = rg < a.rows;
-    const int rlane = rg / lane_rows, trow = rg % lane_rows;
-    float M = -INFINITY, L = 0.0f, acc[E];
-    bool lost = false;  // a partial that did not come in time is among them
+    const int W = join_warps(g1 - g0 + 1), per = kJoinWarps / W;
+#pragma unroll 1
+    for (int row0 = blockIdx.y * per; row0 < a.rows; row0 += gridDim.y * per) {
+        const int rg = row0 + warp / W;
+        const bool row_ok = rg < a.rows;
+        const int rlane = rg / lane_rows, trow = rg % lane_rows;
+        float M = -INFINITY, L = 0.0f, acc[E];
+        bool lost = false;  // a partial that did not come in time is among them
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-    if (row_ok) {
-        for (int gb = g0 + warp % W; gb <= g1; gb += U * W) {
-            float m[U], l[U], o[U][E];
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+        if (row_ok) {
+            for (int gb = g0 + warp % W; gb <= g1; gb += U * W) {
+                float m[U], l[U], o[U][E];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                const int g = gb + k * W;
-                m[k] = -INFINITY;
-                l[k] = 0.0f;
+                for (int k = 0; k < U; ++k) {
+                    const int g = gb + k * W;
+                    m[k] = -INFINITY;
+                    l[k] = 0.0f;
 #pragma unroll
-                for (int i = 0; i < E; ++i) o[k][i] = 0.0f;
-                if (g <= g1) {
-                    // (ranges between the first and the last are never empty)
-                    const int64_t pr = ((int64_t)(g * a.lanes + rlane) * 2 + (u0 > deal.start(g))) * lane_rows + trow;
-                    const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + pr * 2);
-                    m[k] = ml.x;
-                    l[k] = ml.y;
-                    const float *src = a.ws_o + pr * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 q = *reinterpret_cast<const float4 *>(src);
-                        o[k][0] = q.x; o[k][1] = q.y; o[k][2] = q.z; o[k][3] = q.w;
-                    } else {
-                        const float2 q = *reinterpret_cast<const float2 *>(src);
-                        o[k][0] = q.x; o[k][1] = q.y;
+                    for (int i = 0; i < E; ++i) o[k][i] = 0.0f;
+                    if (g <= g1) {
+                        // (ranges between the first and the last are never empty)
+                        const int64_t pr = ((int64_t)(g * a.lanes + rlane) * 2 + (u0 > deal.start(g))) * lane_rows + trow;
+                        const float2 ml = *reinterpret_cast<const float2 *>(a.ws_ml + pr * 2);
+                        m[k] = ml.x;
+                        l[k] = ml.y;
+                        const float *src = a.ws_o + pr * D + lane * E;
+                        if constexpr (E == 4) {
+                            const float4 q = *reinterpret_cast<const float4 *>(src);
+                            o[k][0] = q.x; o[k][1] = q.y; o[k][2] = q.z; o[k][3] = q.w;
+                        } else {
+                            const float2 q = *reinterpret_cast<const float2 *>(src);
+                            o[k][0] = q.x; o[k][1] = q.y;
+                        }
                     }
                 }
-            }
-            float mx = M;
+                float mx = M;
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                mx = fmaxf(mx, m[k]);
-                lost |= l[k] < 0.0f;
-            }
-            if (mx == -INFINITY) continue;
-            const float f = ex2(M - mx);
-            M = mx;
-            L *= f;
+                for (int k = 0; k < U; ++k) {
+                    mx = fmaxf(mx, m[k]);
+                    lost |= l[k] < 0.0f;
+                }
+                if (mx == -INFINITY) continue;
+                const float f = ex2(M - mx);
+                M = mx;
+                L *= f;
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] *= f;
+                for (int i = 0; i < E; ++i) acc[i] *= f;
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (m[k] == -INFINITY) continue;  // (nothing seen there)
-                const float wk = ex2(m[k] - mx) * l[k];
-                L += wk;
+                for (int k = 0; k < U; ++k) {
+                    if (m[k] == -INFINITY) continue;  // (nothing seen there)
+                    const float wk = ex2(m[k] - mx) * l[k];
+                    L += wk;
 #pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(wk, o[k][i], acc[i]);
+                    for (int i = 0; i < E; ++i) acc[i] = fmaf(wk, o[k][i], acc[i]);
+                }
             }
         }
-    }
-    if (W > 1) {
-        part[warp][0][lane] = M;
-        part[warp][1][lane] = lost ? -1.0f : L;
+        if (W > 1) {
+            __syncthreads();  // (the rows before have been read)
+            part[warp][0][lane] = M;
+            part[warp][1][lane] = lost ? -1.0f : L;
 #pragma unroll
-        for (int i = 0; i < E; ++i) part[warp][2 + i][lane] = acc[i];
-        __syncthreads();
-        if (warp % W) return;
-        for (int k = 1; k < W; ++k) {
-            const float m = part[warp + k][0][lane], mx = fmaxf(M, m);
-            lost |= part[warp + k][1][lane] < 0.0f;
-            if (m == -INFINITY) continue;
-            const float f = ex2(M - mx), wk = ex2(m - mx);
-            M = mx;
-            L = L * f + part[warp + k][1][lane] * wk;
+            for (int i = 0; i < E; ++i) part[warp][2 + i][lane] = acc[i];
+            __syncthreads();
+            if (warp % W) continue;
+            for (int k = 1; k < W; ++k) {
+                const float m = part[warp + k][0][lane], mx = fmaxf(M, m);
+                lost |= part[warp + k][1][lane] < 0.0f;
+                if (m == -INFINITY) continue;
+                const float f = ex2(M - mx), wk = ex2(m - mx);
+                M = mx;
+                L = L * f + part[warp + k][1][lane] * wk;
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + part[warp + k][2 + i][lane] * wk;
+                for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + part[warp + k][2 + i][lane] * wk;
+            }
         }
-    }
-    if (!row_ok) return;
-    const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
-    const bool zero = lost || M == -INFINITY;
-    const float f = zero ? 0.0f : 1.0f / L;
+        if (!row_ok) continue;
+        const int64_t orow = ((int64_t)b * a.n_q + rg / a.grp) * a.hq + (int64_t)kvh * a.grp + rg % a.grp;
+        const bool zero = lost || M == -INFINITY;
+        const float f = zero ? 0.0f : 1.0f / L;
 #pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = zero ? 0.0f : acc[i] * f;
-    if (a.out_bf16) {
-        uint32_t *dst = reinterpret_cast<uint32_t *>((uint16_t *)a.out + orow * D + lane * E);
+        for (int i = 0; i < E; ++i) acc[i] = zero ? 0.0f : acc[i] * f;
+        if (a.out_bf16) {
+            uint32_t *dst = reinterpret_cast<uint32_t *>((uint16_t *)a.out + orow * D + lane * E);
 #pragma unroll
-        for (int i = 0; i < E / 2; ++i) dst[i] = pack_bf16(acc[2 * i], acc[2 * i + 1]);
-    } else {
+            for (int i = 0; i < E / 2; ++i) dst[i] = pack_bf16(acc[2 * i], acc[2 * i + 1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < E; ++i) ((float *)a.out)[orow * D + lane * E + i] = acc[i];
+            for (int i = 0; i < E; ++i) ((float *)a.out)[orow * D + lane * E + i] = acc[i];
+        }
     }
 }
 

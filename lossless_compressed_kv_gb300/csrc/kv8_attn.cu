@@ -33,9 +33,9 @@ __global__ void __launch_bounds__(kv8::Tc<D, QT>::THREADS, 1) kv8_tc_kernel(cons
 
 template <int D, int BK>
 __global__ void __launch_bounds__(kv8::kJoinWarps * 32)
-    kv8_join_kernel(const __grid_constant__ kv8::Args a, int warps_per_row, int lane_rows) {
+    kv8_join_kernel(const __grid_constant__ kv8::Args a, int lane_rows) {
     pdl_begin();
-    kv8::join_block<D, BK>(a, warps_per_row, lane_rows);
+    kv8::join_block<D, BK>(a, lane_rows);
 }
 
 bool supported(const vc_paged_kv8 &kv, int n_q, int hq) {
@@ -82,10 +82,11 @@ size_t workspace_of(const Plan &p, int d) { return (size_t)p.slots() * (d + 2) *
 
 template <int D, int BK>
 cudaError_t launch_join(const kv8::Args &a, int lane_rows, cudaStream_t st) {
-    // ranges that a unit spans, were the lengths alike: a warp reads eight at once
-    const int ranges = a.groups / (a.batch * a.hkv), W = ranges < 8 ? 1 : ranges < 16 ? 2 : ranges < 32 ? 4 : 8;
-    const dim3 grid(a.batch * a.hkv, ceil_div(a.rows, kv8::kJoinWarps / W));
-    const cudaError_t e = launch_pdl(kv8_join_kernel<D, BK>, grid, kv8::kJoinWarps * 32, 0, st, a, W, lane_rows);
+    // blocks for a go through all rows, were the lengths alike; a few more for a unit that
+    // spans more ranges than the others
+    const int W = kv8::join_warps(a.groups / (a.batch * a.hkv)), some = ceil_div(a.rows, kv8::kJoinWarps / W);
+    const dim3 grid(a.batch * a.hkv, some < 4 ? (a.rows < 4 ? a.rows : 4) : some);
+    const cudaError_t e = launch_pdl(kv8_join_kernel<D, BK>, grid, kv8::kJoinWarps * 32, 0, st, a, lane_rows);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 template <int D, int NT, bool E4M3>
