@@ -816,7 +816,7 @@ VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, con
  * 16 rows of a kv head, 32 with head_dim 64; fewer are served without waits).
  * Codes are exact in the products' type (fp16), and q is taken times a power
  * of two for each row that fits it there; probabilities enter the second product in fp16
- * (each off by at most 2^-11 of itself, or 2^-25 of the largest beside V's
+ * (each off by at most 2^-11 of itself, or 2^-32 of the largest beside V's
  * largest scale).  Everything else is fp32.  The context is split evenly over
  * the GPU, so the last bits of a result depend on the batch's lengths; they
  * are the same from call to call.

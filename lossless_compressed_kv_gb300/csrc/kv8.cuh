@@ -5,9 +5,12 @@
 // Both codes are exact in fp16 (e4m3 by definition, whole numbers up to 127),
 // so the products run on codes and the scales stand outside: K's beside the
 // softmax scale, a factor a page, and V's beside the probability.  A
-// probability times V's scale goes to fp16 relative to a reference that is not
-// below any scale met so far, so that it neither overflows nor, unless it adds
-// less than 2^-24 of what the largest would, gets lost.  Q is bf16 and goes to
+// probability times V's scale goes to fp16 relative to a reference that is
+// twice the largest scale met so far, and the probability relative to one that
+// lies 2^8 to 2^16 below the largest (kBelow, kRise): stored values reach 2^15,
+// of fp16's 2^16, and the largest is at least 2^7, so one of which that is off by
+// half the smallest step, 2^-25, is off by at most 2^-32 of the largest beside
+// V's largest scale.  Q is bf16 and goes to
 // fp16 by a power of two that puts a row's largest value at 2^8: what lies
 // within 2^25 of it keeps all its bits.
 //
@@ -72,6 +75,10 @@ template <bool E4M3>
 __device__ __forceinline__ uint32_t raw(uint32_t w) {
     return E4M3 ? w : w ^ 0x80808080u;
 }
+
+// A row's reference for its probabilities 2^(score - reference): set kBelow below
+// the largest score met, and again once one lies kRise above it.
+constexpr float kBelow = 8.0f, kRise = 16.0f;
 
 // A scale, or the nearer end of what scales may be (NaN: the lower).
 __device__ __forceinline__ float scale_of(float s) { return fminf(fmaxf(s, 0x1p-126f), 0x1p122f); }

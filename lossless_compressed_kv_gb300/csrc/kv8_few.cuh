@@ -226,11 +226,11 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                         if (!((seen >> (g + 8)) & 1)) x[n][c + 2] = -INFINITY;
                     }
             }
-            // (the reference maximum follows only rises of more than 2^8)
+            // (the reference of a row's maximum follows only rises beyond kRise)
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) grow |= x[n][c] > m[n][c & 1] + 8.0f;
+                for (int c = 0; c < 4; ++c) grow |= x[n][c] > m[n][c & 1] + kRise;
             if (__any_sync(0xffffffffu, grow)) {
                 // V's reference: twice the largest scale so far
                 float fv = 1.0f;
@@ -248,7 +248,8 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                         float f = 1.0f;
-                        if (mx > m[n][c] + 8.0f) {
+                        if (mx > m[n][c] + kRise) {
+                            mx -= kBelow;
                             f = ex2(m[n][c] - mx);
                             m[n][c] = mx;
                         }

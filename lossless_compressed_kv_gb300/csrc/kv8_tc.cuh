@@ -469,11 +469,11 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
                     mb = fmaxf(mb, tree::max_of<16>(*reinterpret_cast<float(*)[16]>(&s[16 * p])) * kf);
                     vtop = fmaxf(vtop, f.y);
                 }
-                // the reference maximum follows only rises of more than 2^8, V's
-                // reference is twice the largest scale so far; then O is rescaled
-                const bool grow = mb > m_used + 8.0f, more = vtop > vref;
+                // the reference of a row's maximum follows only rises beyond kRise, V's
+                // is twice the largest scale so far; then O is rescaled
+                const bool grow = mb > m_used + kRise, more = vtop > vref;
                 if (__any_sync(0xffffffffu, grow || more)) {
-                    float f = grow ? (m_used == -INFINITY ? 0.0f : ex2(m_used - mb)) : 1.0f;
+                    float f = grow ? (m_used == -INFINITY ? 0.0f : ex2(m_used - (mb - kBelow))) : 1.0f;
                     l *= f;
                     if (more) {
                         inv_vref = 0.5f / vtop;
@@ -496,7 +496,7 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
                         }
                     }
                 }
-                if (grow) m_used = mb;
+                if (grow) m_used = mb - kBelow;
                 const float nms = m_used == -INFINITY ? 0.0f : -m_used;
                 float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

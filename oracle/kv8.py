@@ -58,9 +58,9 @@ def attn(q, k, v, seen, scale, v_top):
     Returns (out [rows][d], bound of the kernel's error beside it).
 
     The bound: a probability enters the second product in fp16, off by half a
-    step, 2^-11 of itself, or by 2^-25 of the reference where it is smaller than
-    fp16's normal numbers (the reference is at most twice the largest scale, and
-    the largest probability at least 1 before division by their sum).  A score
+    step, 2^-11 of itself, or by 2^-25 where it is smaller than fp16's normal
+    numbers, of values that are relative to at most twice the largest scale and
+    in which the largest probability is at least 2^8.  A score
     is a sum of head_dim products in fp32: off by at most D 2^-23 of sum |q k|
     scale; and by 2^-21 of itself and of the maximum for the factors and the
     subtraction, each of which moves p by as much relatively, in numerator and
@@ -79,5 +79,5 @@ def attn(q, k, v, seen, scale, v_top):
     spread = (p @ np.abs(v)) / ln
     d = q.shape[1]
     shift = np.where(seen, mag, 0.0).max(-1, keepdims=True) * (d * 2.0 ** -23 + 2.0 ** -20)
-    few = 2.0 ** -25 * 2.0 * v_top * (p > 0).sum(-1, keepdims=True) / ln
+    few = 2.0 ** -25 * 2.0 / 2.0 ** 8 * v_top * (p > 0).sum(-1, keepdims=True) / ln
     return out, spread * (2.0 ** -11 + 2.0 ** -12 + 2 * shift) + few
