@@ -814,6 +814,7 @@ VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, con
  * pages, gets zeros and VC_ERR_BAD_INDEX; a row whose keys did not all arrive
  * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT (more than
  * 16 rows of a kv head, 32 with head_dim 64; fewer are served without waits).
+ * Scores are fp32, in base 2: a row that sees one beyond its range is void.
  * Codes are exact in the products' type (fp16), and q is taken times a power
  * of two for each row that fits it there; probabilities enter the second product in fp16
  * (each off by at most 2^-11 of itself, or 2^-32 of the largest beside V's

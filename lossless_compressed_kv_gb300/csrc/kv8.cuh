@@ -83,6 +83,10 @@ constexpr float kBelow = 8.0f, kRise = 16.0f;
 // A scale, or the nearer end of what scales may be (NaN: the lower).
 __device__ __forceinline__ float scale_of(float s) { return fminf(fmaxf(s, 0x1p-126f), 0x1p122f); }
 
+// A row's factor beside K's scale, kept finite (a score of 0 stays 0) and not 0
+// (it meets the masked scores' infinity; 2^-126 more moves no score by 2^-100).
+__device__ __forceinline__ float factor_of(float k_scale, float rf) { return fminf(fmaf(k_scale, rf, 0x1p-126f), 0x1p127f); }
+
 // The power of two that takes a row whose largest magnitude is `amax` to 2^8.
 __device__ __forceinline__ int q_exponent(float amax) {
     const int e = (int)(__float_as_uint(amax) >> 23 & 255) - 127;

@@ -213,7 +213,7 @@ __device__ __forceinline__ void few_warp(const Args &a, uint8_t *smem) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) x[n][c] *= sc2.x * rf[n][c & 1];
+                for (int c = 0; c < 4; ++c) x[n][c] *= factor_of(sc2.x, rf[n][c & 1]);
             if (key0 + BK > base) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)

@@ -450,8 +450,7 @@ __device__ __forceinline__ void one_cta(const Args &a, uint8_t *smem) {
 #pragma unroll
                 for (int p = 0; p < PG; ++p) {
                     const float2 f = sc[p];
-                    // (not 0: it meets the masked scores' infinity)
-                    kf[p] = fmaxf(f.x * rf, 0x1p-126f);
+                    kf[p] = factor_of(f.x, rf);
                     vw[p] = f.y;
                     mb = fmaxf(mb, tree::max_of<16>(*reinterpret_cast<float(*)[16]>(&s[16 * p])) * kf[p]);
                     vtop = fmaxf(vtop, f.y);

@@ -464,8 +464,7 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
 #pragma unroll
                 for (int p = 0; p < PG; ++p) {
                     const float2 f = sc[p];
-                    // (not 0: it meets the masked scores' infinity)
-                    const float kf = fmaxf(f.x * rf, 0x1p-126f);
+                    const float kf = factor_of(f.x, rf);
                     mb = fmaxf(mb, tree::max_of<16>(*reinterpret_cast<float(*)[16]>(&s[16 * p])) * kf);
                     vtop = fmaxf(vtop, f.y);
                 }
@@ -505,7 +504,7 @@ __device__ __forceinline__ void tc_cta(const Args &a, uint8_t *smem) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
                         const float2 f = sc[2 * h + p];
-                        const float kf = fmaxf(f.x * rf, 0x1p-126f), vw = f.y * inv_vref;
+                        const float kf = factor_of(f.x, rf), vw = f.y * inv_vref;
 #pragma unroll
                         for (int c = 8 * p; c < 8 * p + 8; ++c) {
                             float p0, p1;
