@@ -74,7 +74,7 @@ Plan plan_of(const vc_paged_kv8 &kv, int n_q, int hq, int max_seq_len) {
         most = tree::kSMs / p.lanes;
         block = kv8::One<128>::BK;
     }
-    const int64_t blocks = (int64_t)kv.batch * kv.num_kv_heads * ceil_div(max_seq_len, block);
+    const int64_t blocks = (int64_t)kv.batch * kv.num_kv_heads * (((int64_t)max_seq_len + block - 1) / block);
     p.groups = (int)(blocks < 1 ? 1 : blocks < most ? blocks : most);
     return p;
 }
@@ -158,9 +158,11 @@ vc_status vc_kv8_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc_
     const float scale_log2 = softmax_scale * 1.4426950408889634f;
     if (!supported(*kv, n_q, num_q_heads) || (out_dtype != VC_F32 && out_dtype != VC_BF16) || !std::isfinite(scale_log2))
         return VC_ERR_UNSUPPORTED;
-    // (the kernels count the pages of a call, and the rows of a pool, in 32 bits)
+    // (the kernels count keys, the pages of a call, and the rows of a pool, in 32 bits)
     const int64_t held = (int64_t)kv->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
-    if ((longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX || kv->num_pages > INT32_MAX / kPage / kv->num_kv_heads) return VC_ERR_UNSUPPORTED;
+    if (longest > INT32_MAX - 128 || (longest / kPage + 1) * kv->batch * kv->num_kv_heads > INT32_MAX ||
+        kv->num_pages > INT32_MAX / kPage / kv->num_kv_heads)
+        return VC_ERR_UNSUPPORTED;
     if (kv->batch == 0) return VC_OK;
     if (!q || !out || !kv8_ok(kv) || !kv->seq_lens || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) || ((uintptr_t)workspace & 31))
         return VC_ERR_INVALID_ARG;

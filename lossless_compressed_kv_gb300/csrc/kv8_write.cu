@@ -32,7 +32,7 @@ struct WriteArgs {
 __device__ inline int pages_of(const WriteArgs &a, int b) {
     const int len = a.lens[b], first = a.first ? a.first[b] : 0;
     if (first < 0 || len < 0 || len > a.max_len) return 0;
-    return first >= len ? 0 : ceil_div(len, kPage) - first / kPage;
+    return first >= len ? 0 : (len - 1) / kPage + 1 - first / kPage;
 }
 
 // The request whose tokens page `dst`, the pg-th of request b, is made of: the
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) kv8_write_kernel(const __grid_
 
 template <int D, bool E4M3>
 cudaError_t launch(const WriteArgs &a, cudaStream_t st) {
-    const int64_t most = ((int64_t)a.batch * ceil_div(a.max_len, kPage) * a.hkv * 2 + kWarps - 1) / kWarps;
+    const int64_t most = ((int64_t)a.batch * (a.max_len / kPage + 1) * a.hkv * 2 + kWarps - 1) / kWarps;
     const int full = 152 * 4;
     return launch_pdl(kv8_write_kernel<D, E4M3>, (int)(most < 1 ? 1 : most < full ? most : full), kWarps * 32, 0, st, a);
 }
