@@ -527,11 +527,11 @@ vc_status vc_pages_compact(const vc_page_map *map, int32_t *move_src, int32_t *m
                            int32_t *dev_status, vc_stream_t stream) {
     // (no more pages can move than half the pool: each leaves one id for another)
     if (!map_sizes_ok(map) || max_moves < map->num_pages / 2) return VC_ERR_INVALID_ARG;
-    if (map->num_pages == 0) return VC_OK;
-    if (!map->refs || (map->batch > 0 && !map_ok(map)) || (max_moves > 0 && (!move_src || !move_dst)) || !moves ||
-        !remap || ((uintptr_t)workspace & 3))
+    if ((max_moves > 0 && (!move_src || !move_dst)) || !moves) return VC_ERR_INVALID_ARG;
+    const bool none = map->num_pages == 0;  // (no moves, and that is said)
+    if (!none && (!map->refs || (map->batch > 0 && !map_ok(map)) || !remap || ((uintptr_t)workspace & 3)))
         return VC_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < workspace_of(map)) return VC_ERR_WORKSPACE;
+    if (!none && (!workspace || workspace_bytes < workspace_of(map))) return VC_ERR_WORKSPACE;
     Compact a;
     a.m = map_of(map);
     a.src = move_src;
@@ -551,7 +551,7 @@ vc_status vc_pages_compact(const vc_page_map *map, int32_t *move_src, int32_t *m
         if (e == cudaSuccess) e = launch_pdl(pages_rank_kernel, chunks, kThreads, 0, st, a);
         if (e == cudaSuccess) e = launch_pdl(pages_move_kernel, min(ceil_div((int)(map->num_pages / 2) + 1, 256), 304), 256, 0, st, a);
     }
-    if (e == cudaSuccess && map->batch > 0) e = launch_pdl(pages_rename_kernel, map->batch, 256, 0, st, a);
+    if (e == cudaSuccess && map->batch > 0 && !none) e = launch_pdl(pages_rename_kernel, map->batch, 256, 0, st, a);
     return done(e);
 }
 
