@@ -854,26 +854,31 @@ def _map(m: PageMap, dev: int) -> PageMapStruct:
 
 class PageArrays:
     """Tensors whose first axis is a pool's pages (K and V pools of any format,
-    scales), as vc_pages_copy takes them; built once, kept by the caller."""
+    scales), as vc_pages_copy takes them; built once, kept by the caller.  One
+    that was moved or resized in place is read anew."""
 
     def __init__(self, tensors):
         self.tensors = tuple(tensors)
-        n = {int(t.shape[0]) for t in self.tensors}
-        if len(n) > 1:
-            raise ValueError("all arrays hold the same pages")
-        self.num_pages = n.pop() if n else 0
         self._read(_device())
 
     def _read(self, dev):
+        pages = {t.shape[0] for t in self.tensors}
+        if len(pages) > 1:
+            raise ValueError("all arrays hold the same pages")
+        n = pages.pop() if pages else 0
         for t in self.tensors:
             if not t.is_contiguous():
                 raise ValueError("arrays of pages must be contiguous")
-        self.structs = (PageArrayStruct * len(self.tensors))(
-            *[PageArrayStruct(_here("array", t, dev), t.nbytes // max(1, self.num_pages)) for t in self.tensors])
-        self.device = dev
+        structs = (PageArrayStruct * len(self.tensors))(
+            *[PageArrayStruct(_here("array", t, dev), t.nbytes // max(1, n)) for t in self.tensors])
+        self._held = [(t, t.data_ptr(), t.shape) for t in self.tensors]
+        self.device, self.num_pages, self.structs = dev, n, structs
 
     def _as_read(self) -> bool:
-        return all(t.data_ptr() == s.data for t, s in zip(self.tensors, self.structs))
+        for t, p, shape in self._held:
+            if t.data_ptr() != p or t.shape != shape:
+                return False
+        return True
 
 
 def pages_workspace_bytes(pages: PageMap) -> int:
