@@ -352,9 +352,10 @@ __global__ void __launch_bounds__(kThreads) pages_rank_kernel(const __grid_const
 }
 
 // The same by one block, the moves' marks included, for pools of up to
-// kSmallPool pages: 1024 pages 5.2 us where three launches take 9.0, 8192 pages
-// 10.2 and 10.7, 16384 pages 15.4 and 11.5.
-constexpr int kSmallPool = 4096;
+// kSmallPool pages, a third of them free: 1024 pages 5.0 us where three launches
+// take 9.0, 4096 pages 7.4 and 10.8, 8192 pages 10.2 and 11.4, 12000 pages 13.6
+// and 12.8, 16384 pages 16.0 and 12.3.
+constexpr int kSmallPool = 8192;
 __global__ void __launch_bounds__(kThreads) pages_rank_small_kernel(const __grid_constant__ Compact a) {
     pdl_begin();
     __shared__ int warps[32];
