@@ -651,7 +651,7 @@ VC_API vc_status vc_tree_plan(const int32_t *parent, int32_t batch, int32_t n_q,
  * whatever they hold (infinities and NaN included); a node that attends to an
  * entry of the tree whose V holds one gets NaN in all channels.  The context
  * is split evenly over the GPU, so the last bits of a result depend on the
- * batch's lengths; they are the same from call to call.
+ * batch's lengths and on max_seq_len; they are the same from call to call.
  */
 VC_API size_t vc_tree_workspace_bytes(const vc_paged_kv *full, int32_t n_q, int32_t num_q_heads,
                                       int32_t max_seq_len);

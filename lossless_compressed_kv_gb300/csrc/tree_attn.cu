@@ -31,7 +31,8 @@ struct Plan {
 };
 Plan plan_of(const vc_paged_kv &f, int n_q, int hq, int max_seq_len) {
     const int tiles = ceil_div(n_q * (hq / f.fmt.num_kv_heads), tree::kTileRows), lanes = tiles == 4 ? 2 : 1;
-    const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * ceil_div(max_seq_len, tree::Cfg<128, 1>::BK);
+    constexpr int BK = tree::Cfg<128, 1>::BK;
+    const int64_t blocks = (int64_t)f.batch * f.fmt.num_kv_heads * (((int64_t)max_seq_len + BK - 1) / BK);
     const int most = (tiles == 1 ? 2 * tree::kSMs : tree::kSMs) / lanes;
     return {tiles / lanes, lanes, (int)(blocks < 1 ? 1 : blocks < most ? blocks : most)};
 }
@@ -73,9 +74,10 @@ vc_status vc_tree_attn(const void *q, int32_t n_q, int32_t num_q_heads, const vc
     if (!verify_supported(full->fmt, num_q_heads, n_q) || (out_dtype != VC_F32 && out_dtype != VC_BF16) ||
         !std::isfinite(scale_log2))
         return VC_ERR_UNSUPPORTED;
-    // (the kernel counts blocks in 32 bits)
+    // (the kernel counts keys and blocks in 32 bits)
     const int64_t held = (int64_t)full->max_blocks * kPage, longest = held < max_seq_len ? held : max_seq_len;
-    if ((longest / tree::Cfg<128, 1>::BK + 1) * full->batch * full->fmt.num_kv_heads > INT32_MAX)
+    if (longest > INT32_MAX - 128 ||
+        (longest / tree::Cfg<128, 1>::BK + 1) * full->batch * full->fmt.num_kv_heads > INT32_MAX)
         return VC_ERR_UNSUPPORTED;
     if (full->batch == 0) return VC_OK;
     if (!q || !mask || !out || !paged_ok(full) || ((uintptr_t)q & 15) || ((uintptr_t)out & 15) ||
