@@ -814,6 +814,9 @@ VC_API vc_status vc_kv8_write(const vc_paged_kv *full, const int32_t *first, con
  * pages, gets zeros and VC_ERR_BAD_INDEX; a row whose keys did not all arrive
  * within the time limit of the kernel's waits zeros and VC_ERR_TIMEOUT (more than
  * 16 rows of a kv head, 32 with head_dim 64; fewer are served without waits).
+ * Half the bytes of KV_full make it faster where they bound it; with many rows
+ * the widening of codes does, and vc_tree_attn over KV_full takes less time
+ * (more than 128 rows, with head_dim 64 more than 16).
  * Scores are fp32, in base 2: a row that sees one beyond its range is void.
  * Codes are exact in the products' type (fp16), and q is taken times a power
  * of two for each row that fits it there; probabilities enter the second product in fp16
@@ -898,7 +901,8 @@ VC_API vc_status vc_pages_fork(const vc_page_map *map, int32_t *seq_lens, const 
  *            (on this stream, before the row is written to); -1 where there
  *            is none
  * A row of impossible lengths (negative, more tokens than its pages hold, more
- * than max_blocks) or bad pages is left as it was, not granted and reported
+ * than max_blocks) or bad pages (out of range, or that nobody holds as the call
+ * finds the map) is left as it was, not granted and reported
  * (VC_ERR_BAD_INDEX).  seq_lens is not changed.
  */
 VC_API vc_status vc_pages_reserve(const vc_page_map *map, const int32_t *seq_lens, const int32_t *want,

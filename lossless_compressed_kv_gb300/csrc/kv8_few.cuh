@@ -14,7 +14,7 @@
 // rows that are not there (kv8_one.cuh takes 155 us for four rows), while these
 // spend an instruction on 128 codes.
 // 8 x 32768 keys, 8 heads of 128: 4 rows 98 us (0.81 of measured HBM), 16 rows
-// 112; 4 x 131072 keys, 8 rows 179 (0.89).  Chains of shared-memory loads,
+// 112; 4 x 131072 keys, 8 rows 181 (0.88).  Chains of shared-memory loads,
 // products and conversions bound it: a scheduler's four warps issue in 0.45 of the
 // cycles.
 //

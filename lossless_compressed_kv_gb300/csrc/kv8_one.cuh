@@ -5,14 +5,18 @@
 // maximum, a sum and an O of its own for the same rows: at a segment's end the
 // two are put together.
 //
-// 8 x 32768 keys, 8 heads of 128, 128 rows: 172 us, 80 of which HBM needs; of
-// 4 rows it would take 155.  What bounds it is the warp that issues products
-// (about 50 cycles for each of a block's twelve, 40 for each of four commits, 130
-// for the wait), while the tensor pipe works a third of the time.  Measured
-// against it: two CTAs an SM with a chain of one S buffer each 178 us; codes
-// through a ring filled by TMA 230; S and P V issued by a warp each, which must
-// then wait for one another's products, 222 (head_dim 64: 129, where this takes
-// 130).
+// 8 x 32768 keys, 8 heads of 128, 128 rows: 168 us, 80 of which HBM needs; of
+// 4 rows it would take 155.  By clock reads a block of 64 keys takes a CTA 1250
+// cycles (head_dim 64: 1040), all roles' beginnings and ends of segments dealt out
+// to the blocks.  The warp that issues products works for 770 of them (590): P V
+// 185 (215), S with two commits 480 (300), two commits 105 (75); it waits 190
+// (200) and spends the rest, 290 (250), at segments' ends.  The tensor pipe works a
+// third of the time; a softmax group 1300 of 2530 cycles for a block of its own, a
+// converter 2000 of 4280 for an item.  ptxas spills 280 bytes a thread with 128
+// channels, 8 with 64.  Measured against it: two CTAs an SM with a chain of one S
+// buffer each 178 us; codes through a ring filled by TMA 230; S and P V issued by
+// a warp each, which must then wait for one another's products, 222 (head_dim 64:
+// 129, where this takes 131).
 //
 // Steps are blocks: step i uses S buffer i % NBUF and O i % 2.  A finished
 // S (i) was issued behind P V (i - NBUF): the P V before of the same O, step

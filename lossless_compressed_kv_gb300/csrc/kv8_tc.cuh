@@ -10,7 +10,8 @@
 // What it costs is shared memory: 32 KB of codes (128 keys, head_dim 128) are
 // written, read, written again as 64 KB and read by each tile, with Q: 320 KB for
 // two tiles, 2500 cycles where the products take 2180.
-// 8 x 32768 keys, 256 rows 283 us (1016 TFLOP/s of products), 320 rows 407; seven
+// 8 x 32768 keys, 256 rows 283 us (970 TFLOP/s of products), 320 rows 407 (ptxas
+// spills 160 to 194 bytes a thread); seven
 // warps that fetch codes themselves, as in kv8_one.cuh, took 360 and 448 (the
 // ring of fp16 blocks is then too short, and the softmax warps spill).
 //

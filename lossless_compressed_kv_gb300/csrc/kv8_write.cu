@@ -4,11 +4,12 @@
 // One pass: a warp holds a block (16 rows of K or of V of one kv head) in
 // registers, 16 values a piece, so that the largest magnitude, the scale and
 // the codes come of one read.  Read 2 bytes and written 1 byte a value; HBM
-// bounds it (64750 tokens of 8 heads of 128, K and V: 63 us, 0.94 of measured HBM).  The blocks of all requests, laid end to end, are dealt out in
-// equal ranges to the warps of a grid that fills the GPU once: neighbouring
-// warps take neighbouring heads, and a call with one new page a request costs
-// no more than its pages.  A page that several requests hold is made from the
-// longest of them by each (holder_of).
+// bounds it (64750 tokens of 8 heads of 128, K and V: 63 us, 0.93 of measured
+// HBM).  The blocks of all requests, laid end to end, are dealt out in equal
+// ranges to the warps of a grid that fills the GPU once: neighbouring warps take
+// neighbouring heads, and a call with one new page a request costs little more
+// than its pages (8 requests 3.9 us, 64 6.2, 1000 56).  A page that several
+// requests hold is made from the longest of them by each (holder_of).
 #include "vc_internal.cuh"
 
 namespace vc {
