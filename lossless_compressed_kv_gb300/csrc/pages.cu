@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kThreads) pages_reserve_kernel(const __grid_co
         }
         const int i = k - a.first[lo] - a.anew[lo], p = a.fresh[k];
         if (i < 0) {
-            atomicSub(&m.refs[p], 1);
+            if (atomicSub(&m.refs[p], 1) <= 0) {  // (more rows gave it up than held it: put back)
+                atomicAdd(&m.refs[p], 1);
+                report(a.status, VC_ERR_BAD_INDEX);
+            }
         } else {
             m.table[(int64_t)lo * m.maxb + m.blocks[lo] + i] = p;
             m.refs[p] = 1;

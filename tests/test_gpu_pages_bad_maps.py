@@ -1,8 +1,9 @@
 """GPU page operations on maps that contradict themselves: a row that names a
 page nobody holds is refused, whatever the call does with that page."""
 import pytest
+import torch
 
-from tests.test_gpu_pages import Both
+from tests.test_gpu_pages import Both, i32, vc
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,15 @@ def test_fork_refuses_a_page_that_nobody_holds(n):
     lens[0] = 16 * (n + 2)                       # without that page the row can be shared
     b.fork(lens, [0], [2])
     assert not b.o.bad and lens[2] == lens[0]
+
+
+@pytest.mark.parametrize("rows,refs", [(3, 2), (40, 2), (1500, 700)])
+def test_reserve_of_a_page_that_more_rows_give_up_than_hold_it(rows, refs):
+    """Every row gets a page of its own; the count of the one that they held ends at none and is reported."""
+    b = Both([[0]] * rows, [1] * rows, [refs] + [0] * rows)
+    g, s, d = (i32([7] * rows) for _ in range(3))
+    vc().pages_reserve(b.m, i32([5] * rows), i32([6] * rows), g, s, d, b.ws, status=b.st)
+    torch.cuda.synchronize()
+    assert b.st.item() == 3 and g.tolist() == [1] * rows and s.tolist() == [0] * rows
+    assert d.tolist() == b.m.table[:, 0].tolist() == list(range(1, rows + 1))
+    assert b.m.refs.tolist() == [0] + [1] * rows
